@@ -76,6 +76,7 @@ typedef enum pa_status {
 #define PA_DEVERR_SLOT 0x4      /* an append slot was >= num_blocks*block_size */
 #define PA_DEVERR_TIMEOUT 0x8   /* a bounded pipeline wait gave up (internal error) */
 #define PA_DEVERR_PREFIX 0x10   /* pa_decode_shared_prefix: a group broke its contract (see there) */
+#define PA_DEVERR_POSITION 0x20 /* a token's position was outside [0, max_position) of its rope table */
 
 typedef struct pa_dims {
     int32_t num_seqs;           /* B */
@@ -360,6 +361,115 @@ PA_API pa_status pa_append_decode_fp8(const void* k_new, const void* v_new, cons
 PA_API pa_status pa_prefill(const void* q, const int32_t* cu_q_lens, int32_t max_q_len, const void* k_cache,
                             const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
                             float scale, void* out, const pa_dims* dims, void* stream);
+
+/*
+ * Sliding window with sinks (no counterpart in the pages; decoder layers
+ * with local attention need it).  A query at position p attends to
+ *     t <= p  with  t > p - window  or  t < sinks:
+ * the last `window` tokens, its own included, and the first `sinks` tokens
+ * of the sequence.  window >= 1 (PA_WINDOW_ALL: every token), sinks >= 0,
+ * else PA_ERR_SHAPE.  Only pages that hold a token some query of the call
+ * sees are read, so block-table entries of other pages may hold anything (a
+ * block that slid out of the window can be given away), and so may cached
+ * rows that no query sees.
+ *
+ * pa_decode_window: pa_decode with the window (position p = L_b - 1); the
+ * workspace as for pa_decode.  pa_prefill_window: pa_prefill with the
+ * window.  PA_DECODE_MATH and PA_PREFILL_* do not apply.
+ */
+#define PA_WINDOW_ALL 0x7fffffff
+PA_API pa_status pa_decode_window(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, const int32_t* context_lens, float scale,
+                                  int32_t window, int32_t sinks, void* out, const pa_dims* dims, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+PA_API pa_status pa_prefill_window(const void* q, const int32_t* cu_q_lens, int32_t max_q_len, const void* k_cache,
+                                   const void* v_cache, const int32_t* block_tables, const int32_t* context_lens,
+                                   float scale, int32_t window, int32_t sinks, void* out, const pa_dims* dims,
+                                   void* stream);
+
+/*
+ * 8-bit cache with a scale for each block and kv head (the pages'
+ * quantization theme, MiniVLLM write-up, "量化层"; the scales follow the data
+ * instead of being fixed in advance).  A cached value is code * scale:
+ *   k_cache [NB][Hkv][16][D] int8 and v_cache [NB][Hkv][D][16] int8 (token
+ *            t of a block at byte 4*((t % 8) / 2) + 2*(t / 8) + t % 2 of
+ *            each row), the layouts of the fp8 caches; codes in [-127, 127];
+ *   k_scale, v_scale [NB][Hkv] float32 (device), >= 0.  block_size 16.
+ *
+ * pa_cache_append_i8: the slot-mapped append (as pa_cache_append) of bf16
+ * rows, head_dim 64 or 128.  The call's rows of one block are taken
+ * together, in any order of tokens: per kv head, for K and for V,
+ *     top   = max |x| over those rows,
+ *     old   = the block's scale; 0 if the call writes the block's row 0,
+ *     scale = max(old, top / 127),   code = round(x / scale)
+ * (fp32 division, ties to even; all-zero rows give codes 0).  Writing row 0
+ * starts the block anew: rows the call does not write become 0, so caches
+ * and scales need no initialisation.  Otherwise, when the scale grows, the
+ * block's other codes become round(code * old / scale).  Of two tokens with
+ * one slot the later one lands.  A NaN or infinity poisons its block's
+ * values of that head until the block starts anew.
+ *
+ * pa_decode_i8, pa_prefill_i8: pa_decode and pa_prefill over these caches,
+ * with the window of pa_decode_window (PA_WINDOW_ALL, 0 for none); q must be
+ * finite.  fp32 products, sums and softmax state; the workspace as for
+ * pa_decode.
+ */
+PA_API pa_status pa_cache_append_i8(const void* k_new, const void* v_new, const int32_t* slot_mapping,
+                                    int32_t num_tokens, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                    const pa_dims* dims, void* stream);
+PA_API pa_status pa_decode_i8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                              const float* v_scale, const int32_t* block_tables, const int32_t* context_lens,
+                              float scale, int32_t window, int32_t sinks, void* out, const pa_dims* dims,
+                              void* workspace, size_t workspace_bytes, void* stream);
+PA_API pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_len, const void* k_cache,
+                               const void* v_cache, const float* k_scale, const float* v_scale,
+                               const int32_t* block_tables, const int32_t* context_lens, float scale, int32_t window,
+                               int32_t sinks, void* out, const pa_dims* dims, void* stream);
+
+/*
+ * The step's append with the rotary position embedding on the way (tiny-vllm
+ * write-up, "Chi tiet": RoPE among the forward pass's kernels): one launch
+ * turns the queries into q_out and writes the turned keys and the values to
+ * their slots.  The first rotary_dim values of a q or k row are
+ * rotary_dim / 2 pairs: (x_i, x_{i + rotary_dim/2}), or (x_2i, x_{2i+1}) if
+ * interleaved; pair i of a token at position m becomes
+ *     (a c - b s, b c + a s),  c = cos_sin[m][i],  s = cos_sin[m][rotary_dim/2 + i]
+ * in fp32, rounded once to bf16 (8-bit caches: quantized from fp32).  The
+ * rest of the row and v are copied.
+ *   - q [T][Hq][D], k_new and v_new [T][Hkv][D] bf16 (device): consecutive
+ *     tokens are q_stride, k_stride, v_stride values apart (multiples of 8,
+ *     at least a row), so slices of a fused projection's output need no copy.
+ *     q_out [T][Hq][D] is dense; it may be q itself when q is dense, but must
+ *     not overlap q otherwise (PA_ERR_SHAPE).  q = NULL: keys and values only.
+ *   - positions [T] int32; one outside [0, max_position) sets
+ *     PA_DEVERR_POSITION (row 0 of the table is used).  rotary_dim: a
+ *     multiple of 16, at most D; rope = NULL or rotary_dim = 0 rotates nothing.
+ *   - A token with a negative slot is padding: nothing is read or written for
+ *     it, its q_out row included.  Slots >= NB*bs set PA_DEVERR_SLOT; their
+ *     queries are still turned.
+ *   - Uses dims->num_q_heads, num_kv_heads, head_dim (a multiple of 16; 8-bit
+ *     caches: 64 or 128), block_size, num_blocks.
+ *
+ * pa_rope_append: the bf16 caches of pa_cache_append (of two tokens with one
+ * slot either may land).  pa_rope_append_i8: the 8-bit caches, quantized as
+ * by pa_cache_append_i8.
+ */
+typedef struct pa_rope {
+    const int32_t* positions; /* [T] (device) */
+    const float* cos_sin;     /* [max_position][rotary_dim] (device, 16-byte aligned) */
+    int32_t max_position;
+    int32_t rotary_dim;
+    int32_t interleaved;      /* 0: halves, else neighbours */
+} pa_rope;
+
+PA_API pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                                const void* v_new, int64_t v_stride, const pa_rope* rope,
+                                const int32_t* slot_mapping, int32_t num_tokens, void* q_out, void* k_cache,
+                                void* v_cache, const pa_dims* dims, void* stream);
+PA_API pa_status pa_rope_append_i8(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride,
+                                   const void* v_new, int64_t v_stride, const pa_rope* rope,
+                                   const int32_t* slot_mapping, int32_t num_tokens, void* q_out, void* k_cache,
+                                   void* v_cache, float* k_scale, float* v_scale, const pa_dims* dims, void* stream);
 
 /*
  * Test hook for the bounded waits (no counterpart in the pages).  Every wait

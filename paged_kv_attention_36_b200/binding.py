@@ -22,6 +22,9 @@ PA_DEVERR_CONTEXT = 0x2
 PA_DEVERR_SLOT = 0x4
 PA_DEVERR_TIMEOUT = 0x8
 PA_DEVERR_PREFIX = 0x10
+PA_DEVERR_POSITION = 0x20
+
+PA_WINDOW_ALL = 0x7FFFFFFF  # a window that holds every token
 
 
 class PaError(RuntimeError):
@@ -73,6 +76,21 @@ def _load(path: str = LIB_PATH):
     lib.pa_append_decode_fp8.restype = i32
     lib.pa_prefill.argtypes = [vp, vp, i32, vp, vp, vp, vp, f32, vp, dp, vp]
     lib.pa_prefill.restype = i32
+    lib.pa_decode_window.argtypes = [vp, vp, vp, vp, vp, f32, i32, i32, vp, dp, vp, sz, vp]
+    lib.pa_decode_window.restype = i32
+    lib.pa_prefill_window.argtypes = [vp, vp, i32, vp, vp, vp, vp, f32, i32, i32, vp, dp, vp]
+    lib.pa_prefill_window.restype = i32
+    lib.pa_cache_append_i8.argtypes = [vp, vp, vp, i32, vp, vp, vp, vp, dp, vp]
+    lib.pa_cache_append_i8.restype = i32
+    lib.pa_decode_i8.argtypes = [vp, vp, vp, vp, vp, vp, vp, f32, i32, i32, vp, dp, vp, sz, vp]
+    lib.pa_decode_i8.restype = i32
+    lib.pa_prefill_i8.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, vp, f32, i32, i32, vp, dp, vp]
+    lib.pa_prefill_i8.restype = i32
+    i64, rp = ctypes.c_int64, ctypes.c_void_p  # rp: a pa_rope* or NULL
+    lib.pa_rope_append.argtypes = [vp, i64, vp, i64, vp, i64, rp, vp, i32, vp, vp, vp, dp, vp]
+    lib.pa_rope_append.restype = i32
+    lib.pa_rope_append_i8.argtypes = [vp, i64, vp, i64, vp, i64, rp, vp, i32, vp, vp, vp, vp, vp, dp, vp]
+    lib.pa_rope_append_i8.restype = i32
     lib.pa_decode_static_ws.argtypes = [vp, vp, vp, vp, vp, f32, vp, dp, vp]
     lib.pa_decode_static_ws.restype = i32
     lib.pa_test_wait_timeout.argtypes = [ctypes.c_int64, vp]
@@ -90,7 +108,9 @@ lib = _load()
 EXPORTS = ("pa_cache_append", "pa_decode_workspace_bytes", "pa_decode_default_ctas", "pa_decode",
            "pa_append_decode", "pa_decode_partials", "pa_decode_static_ws",
            "pa_decode_shared_prefix_workspace_bytes", "pa_decode_shared_prefix", "pa_cache_append_fp8",
-           "pa_decode_fp8", "pa_append_decode_fp8", "pa_prefill", "pa_test_wait_timeout", "pa_device_errors", "pa_status_string")
+           "pa_decode_fp8", "pa_append_decode_fp8", "pa_prefill", "pa_decode_window", "pa_prefill_window",
+           "pa_cache_append_i8", "pa_decode_i8", "pa_prefill_i8", "pa_rope_append", "pa_rope_append_i8",
+           "pa_test_wait_timeout", "pa_device_errors", "pa_status_string")
 
 PA_ERR_SCRATCH_LIMIT = -7
 PA_STATIC_SCRATCH_BYTES = 16 << 20  # include/pa.h
@@ -490,6 +510,246 @@ def prepare_prefill(q, cu_q_lens, max_q_len: int, k_cache, v_cache, block_tables
                   _ptr(context_lens), float(scale), _ptr(out), ctypes.byref(dims), _stream(stream)), "pa_prefill")
     p._keep = (dims, q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out)
     return p
+
+
+# ---- sliding window, 8-bit block-scaled caches, append with rotation ----------
+
+def _same_device(*tensors):
+    """All on the current CUDA device: the C ABI launches there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _window_args(window, sinks):
+    window = PA_WINDOW_ALL if window is None else int(window)
+    sinks = int(sinks)
+    if window < 1 or sinks < 0 or window > PA_WINDOW_ALL or sinks > PA_WINDOW_ALL:
+        raise ValueError("window must be at least 1 (or None), sinks at least 0")
+    return window, sinks
+
+
+def _i8_cache_args(k_cache, v_cache, k_scale, v_scale):
+    _need(k_cache, torch.int8, "k_cache", 4)
+    _need(v_cache, torch.int8, "v_cache", 4)
+    NB, Hkv, bs, D = k_cache.shape
+    if bs != 16 or tuple(v_cache.shape) != (NB, Hkv, D, 16):
+        raise ValueError("8-bit caches are k [NB][Hkv][16][D] and v [NB][Hkv][D][16] (int8)")
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, torch.float32, n, 2)
+        if tuple(t.shape) != (NB, Hkv):
+            raise ValueError(f"{n} must be [NB][Hkv]: one scale per block and kv head")
+    return NB, Hkv, D
+
+
+def _attend(fn, what, q, caches, scales, block_tables, context_lens, scale, window, sinks, out, stream,
+            workspace=None, cu_q_lens=None, max_q_len=None) -> "Prepared":
+    """The windowed and the 8-bit attention calls: checks, then the bound call.
+    A decode has a workspace, a multi-query call cu_q_lens and max_q_len."""
+    window, sinks = _window_args(window, sinks)
+    k_cache, v_cache = caches
+    if scales:
+        _need(q, torch.bfloat16, "q", 3)
+        _need(out, torch.bfloat16, "out", 3)
+        _need(block_tables, torch.int32, "block_tables", 2)
+        _need(context_lens, torch.int32, "context_lens", 1)
+        NB, Hkv, D = _i8_cache_args(k_cache, v_cache, *scales)
+        B = block_tables.shape[0]
+        if out.shape != q.shape or q.shape[2] != D or context_lens.shape[0] != B:
+            raise ValueError("attention shapes disagree")
+        dims = pa_dims(B, q.shape[1], Hkv, D, 16, NB, block_tables.shape[1])
+    if cu_q_lens is None:
+        if not scales:
+            dims = _decode_args(q, k_cache, v_cache, block_tables, context_lens, out)
+        elif q.shape[0] != dims.num_seqs:
+            raise ValueError("a decode has one query row per sequence")
+        if workspace is None:
+            workspace = alloc_workspace(dims, device=q.device)
+        _need(workspace, torch.uint8, "workspace", 1)
+        head, tail = (_ptr(q),), (_ptr(workspace), workspace.numel())
+    else:
+        if not scales:
+            dims = _prefill_args(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out)
+        else:
+            _need(cu_q_lens, torch.int32, "cu_q_lens", 1)
+            if cu_q_lens.shape[0] != dims.num_seqs + 1:
+                raise ValueError("cu_q_lens must have one entry more than there are sequences")
+        head, tail = (_ptr(q), _ptr(cu_q_lens), int(max_q_len)), ()
+    _same_device(q, k_cache, v_cache, *scales, block_tables, context_lens, out, workspace, cu_q_lens)
+    p = Prepared(fn, head + (_ptr(k_cache), _ptr(v_cache)) + tuple(_ptr(t) for t in scales) +
+                 (_ptr(block_tables), _ptr(context_lens), float(scale), window, sinks, _ptr(out),
+                  ctypes.byref(dims)) + tail + (_stream(stream),), what)
+    p._keep = (dims, q, cu_q_lens, k_cache, v_cache, scales, block_tables, context_lens, out, workspace)
+    return p
+
+
+def prepare_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale: float, out, workspace, *,
+                          window, sinks: int = 0, stream=None) -> "Prepared":
+    return _attend(lib.pa_decode_window, "pa_decode_window", q, (k_cache, v_cache), (), block_tables, context_lens,
+                   scale, window, sinks, out, stream, workspace=workspace)
+
+
+def pa_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale: float, out, *, window, sinks: int = 0,
+                     workspace=None, stream=None) -> None:
+    """pa_decode in which a query sees the last ``window`` tokens and the
+    first ``sinks`` tokens of its sequence (see include/pa.h)."""
+    prepare_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, out, workspace, window=window,
+                          sinks=sinks, stream=stream)()
+
+
+def prepare_prefill_window(q, cu_q_lens, max_q_len: int, k_cache, v_cache, block_tables, context_lens, scale: float,
+                           out, *, window, sinks: int = 0, stream=None) -> "Prepared":
+    return _attend(lib.pa_prefill_window, "pa_prefill_window", q, (k_cache, v_cache), (), block_tables, context_lens,
+                   scale, window, sinks, out, stream, cu_q_lens=cu_q_lens, max_q_len=max_q_len)
+
+
+def pa_prefill_window(q, cu_q_lens, max_q_len: int, k_cache, v_cache, block_tables, context_lens, scale: float, out,
+                      *, window, sinks: int = 0, stream=None) -> None:
+    """pa_prefill with the window of pa_decode_window."""
+    prepare_prefill_window(q, cu_q_lens, max_q_len, k_cache, v_cache, block_tables, context_lens, scale, out,
+                           window=window, sinks=sinks, stream=stream)()
+
+
+def prepare_decode_i8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale: float, out,
+                      workspace, *, window=None, sinks: int = 0, stream=None) -> "Prepared":
+    return _attend(lib.pa_decode_i8, "pa_decode_i8", q, (k_cache, v_cache), (k_scale, v_scale), block_tables,
+                   context_lens, scale, window, sinks, out, stream, workspace=workspace)
+
+
+def pa_decode_i8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale: float, out, *,
+                 window=None, sinks: int = 0, workspace=None, stream=None) -> None:
+    """Paged decode over int8 caches with a scale per (block, kv head),
+    ``window=None`` for the whole context (see include/pa.h)."""
+    prepare_decode_i8(q, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, out, workspace,
+                      window=window, sinks=sinks, stream=stream)()
+
+
+def prepare_prefill_i8(q, cu_q_lens, max_q_len: int, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                       scale: float, out, *, window=None, sinks: int = 0, stream=None) -> "Prepared":
+    return _attend(lib.pa_prefill_i8, "pa_prefill_i8", q, (k_cache, v_cache), (k_scale, v_scale), block_tables,
+                   context_lens, scale, window, sinks, out, stream, cu_q_lens=cu_q_lens, max_q_len=max_q_len)
+
+
+def pa_prefill_i8(q, cu_q_lens, max_q_len: int, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                  scale: float, out, *, window=None, sinks: int = 0, stream=None) -> None:
+    """pa_prefill over int8 caches with a scale per (block, kv head)."""
+    prepare_prefill_i8(q, cu_q_lens, max_q_len, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens,
+                       scale, out, window=window, sinks=sinks, stream=stream)()
+
+
+class pa_rope(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p), ("max_position", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+def _rows(t, name, heads, D):
+    """Checks rows [T][heads][D] whose tokens may lie apart; returns the token stride in values."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (heads is not None and tuple(t.shape[1:]) != (heads, D)) or t.shape[2] != D:
+        raise ValueError(f"{name} must be rows [T][heads][{D}], got {tuple(t.shape)}")
+    if t.numel() == 0:
+        return t.shape[1] * D
+    if (t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}'s heads must be dense within a token")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+
+
+def _rope_append(fn, what, q, k_new, v_new, positions, cos_sin, slot_mapping, q_out, caches, scales, interleaved,
+                 stream) -> "Prepared":
+    if scales:
+        NB, Hkv, D = _i8_cache_args(*caches, *scales)
+        bs = 16
+    else:
+        for t, n in zip(caches, ("k_cache", "v_cache")):
+            _need(t, torch.bfloat16, n, 4)
+        if caches[0].shape != caches[1].shape:
+            raise ValueError("append shapes disagree")
+        NB, Hkv, bs, D = caches[0].shape
+    _need(slot_mapping, torch.int32, "slot_mapping", 1)
+    T = slot_mapping.shape[0]
+    ks, vs = _rows(k_new, "k_new", Hkv, D), _rows(v_new, "v_new", Hkv, D)
+    qs, Hq = 0, Hkv
+    if q is not None:
+        qs, Hq = _rows(q, "q", None, D), q.shape[1]
+        _need(q_out, torch.bfloat16, "q_out", 3)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    if k_new.shape[0] != T or v_new.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("q, k_new, v_new and slot_mapping must have one row per token")
+    rope = None
+    if cos_sin is not None:
+        _need(cos_sin, torch.float32, "cos_sin", 2)
+        _need(positions, torch.int32, "positions", 1)
+        if positions.shape[0] != T:
+            raise ValueError("positions must have one entry per token")
+        rope = pa_rope(positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                       int(bool(interleaved)))
+    _same_device(q, k_new, v_new, positions, cos_sin, slot_mapping, q_out, *caches, *scales)
+    dims = pa_dims(0, Hq, Hkv, D, bs, NB, 0)
+    p = Prepared(fn, (_ptr(q), qs, _ptr(k_new), ks, _ptr(v_new), vs,
+                      ctypes.byref(rope) if rope is not None else None, _ptr(slot_mapping), T, _ptr(q_out)) +
+                 tuple(_ptr(t) for t in (*caches, *scales)) + (ctypes.byref(dims), _stream(stream)), what)
+    p._keep = (dims, rope, q, k_new, v_new, positions, cos_sin, slot_mapping, q_out, caches, scales)
+    return p
+
+
+def prepare_rope_append(q, k_new, v_new, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, *,
+                        interleaved: bool = False, stream=None) -> "Prepared":
+    return _rope_append(lib.pa_rope_append, "pa_rope_append", q, k_new, v_new, positions, cos_sin, slot_mapping,
+                        q_out, (k_cache, v_cache), (), interleaved, stream)
+
+
+def pa_rope_append(q, k_new, v_new, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, *,
+                   interleaved: bool = False, stream=None) -> None:
+    """q_out = q turned by its positions' angles, k_cache/v_cache[slot] = the
+    turned k_new and v_new.  cos_sin [max_position][rotary_dim] fp32 holds
+    rotary_dim/2 cosines, then as many sines; q, k_new and v_new may be
+    slices of a fused projection (see include/pa.h).  ``q=None``: keys and
+    values only; ``cos_sin=None``: no rotation."""
+    prepare_rope_append(q, k_new, v_new, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache,
+                        interleaved=interleaved, stream=stream)()
+
+
+def prepare_rope_append_i8(q, k_new, v_new, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, k_scale,
+                           v_scale, *, interleaved: bool = False, stream=None) -> "Prepared":
+    return _rope_append(lib.pa_rope_append_i8, "pa_rope_append_i8", q, k_new, v_new, positions, cos_sin,
+                        slot_mapping, q_out, (k_cache, v_cache), (k_scale, v_scale), interleaved, stream)
+
+
+def pa_rope_append_i8(q, k_new, v_new, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, k_scale, v_scale,
+                      *, interleaved: bool = False, stream=None) -> None:
+    """pa_rope_append into int8 caches with a scale per (block, kv head)."""
+    prepare_rope_append_i8(q, k_new, v_new, positions, cos_sin, slot_mapping, q_out, k_cache, v_cache, k_scale,
+                           v_scale, interleaved=interleaved, stream=stream)()
+
+
+def prepare_append_i8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=None) -> "Prepared":
+    NB, Hkv, D = _i8_cache_args(k_cache, v_cache, k_scale, v_scale)
+    for t, n in ((k_new, "k_new"), (v_new, "v_new")):
+        _need(t, torch.bfloat16, n, 3)
+    _need(slot_mapping, torch.int32, "slot_mapping", 1)
+    T = slot_mapping.shape[0]
+    if k_new.shape != v_new.shape or k_new.shape[0] != T or k_new.shape[1:] != (Hkv, D):
+        raise ValueError("k_new/v_new must be [T][Hkv][D] of the cache")
+    _same_device(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale)
+    dims = pa_dims(0, Hkv, Hkv, D, 16, NB, 0)
+    p = Prepared(lib.pa_cache_append_i8,
+                 (_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), T, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                  _ptr(v_scale), ctypes.byref(dims), _stream(stream)), "pa_cache_append_i8")
+    p._keep = (dims, k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale)
+    return p
+
+
+def pa_cache_append_i8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=None) -> None:
+    """Quantize each new bf16 row into its slot of the int8 caches, the scale
+    of each (block, kv head) following its largest value (see include/pa.h)."""
+    prepare_append_i8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream=stream)()
 
 
 def pa_test_wait_timeout(limit_ns: int, stream=None) -> None:

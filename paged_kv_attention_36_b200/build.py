@@ -5,6 +5,7 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -15,8 +16,11 @@ FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden",
-    "-shared",
+    "--split-compile=0",
 ]
+
+# translation units, compiled side by side
+UNITS = ("pa_api.cu", "pa_serving.cu")
 
 
 def sources():
@@ -34,11 +38,19 @@ def stale() -> bool:
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not stale():
         return LIB
-    cmd = [NVCC, *FLAGS, *extra, os.path.join(CSRC, "pa_api.cu"), "-o", LIB]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    print(" ".join(cmd), file=sys.stderr)
-    subprocess.run(cmd, check=True)
+    with tempfile.TemporaryDirectory() as tmp:
+        running, objects = [], []
+        for unit in UNITS:
+            objects.append(os.path.join(tmp, unit + ".o"))
+            cmd = [NVCC, *FLAGS, *extra, "-c", os.path.join(CSRC, unit), "-o", objects[-1]]
+            if verbose:
+                cmd.insert(1, "-Xptxas=-v")
+            print(" ".join(cmd), file=sys.stderr)
+            running.append((cmd, subprocess.Popen(cmd)))
+        failed = [(cmd, p.returncode) for cmd, p in running if p.wait() != 0]
+        if failed:
+            raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
+        subprocess.run([NVCC, *FLAGS[:2], "-shared", *objects, "-o", LIB], check=True)
     return LIB
 
 

@@ -26,7 +26,7 @@ struct AppendParams {
 
 constexpr int kAppendThreads = 256;
 
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) {
+static __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendParams p) {
     const int64_t idx = int64_t(blockIdx.x) * kAppendThreads + threadIdx.x;
     if (idx >= p.num_chunks) return;
     const int64_t per_token = int64_t(p.kv_heads) * p.chunks_per_row;
@@ -117,7 +117,7 @@ __device__ __forceinline__ void append_fp8_chunk(const uint4* k_new, const uint4
     }
 }
 
-__global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(AppendFp8Params p) {
+static __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(AppendFp8Params p) {
     const int64_t idx = int64_t(blockIdx.x) * kAppendThreads + threadIdx.x;
     if (idx >= p.num_chunks) return;
     append_fp8_chunk(p.k_new, p.v_new, p.slot_mapping, p.k_cache, p.v_cache, p.k_scale, p.v_scale, p.kv_heads,

@@ -2,8 +2,8 @@
 // mbarrier arrive/wait (bounded), 1-D bulk async copies (TMA engine),
 // bf16 unpacking, and the device error word.
 //
-// Included by exactly one translation unit (pa_api.cu), so the __device__
-// error word below has a single definition.
+// Included by both translation units; each has an error word of its own, and
+// pa_device_errors() reads and clears the two together.
 #pragma once
 
 #include <cstdint>
@@ -17,7 +17,7 @@
 namespace pa {
 
 // Sticky device error bits (PA_DEVERR_*), read by pa_device_errors().
-__device__ unsigned int g_device_errors;
+static __device__ unsigned int g_device_errors;
 
 __device__ __forceinline__ void raise_error(unsigned int bits) { atomicOr(&g_device_errors, bits); }
 
@@ -139,7 +139,7 @@ __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity, 
 // nothing arrives on, first polling (mbar_wait), then sleeping
 // (mbar_wait_sleep), each for limit_ns; each sets PA_DEVERR_TIMEOUT when it
 // gives up.  Used only by the test hook pa_test_wait_timeout.
-__global__ void wait_timeout_kernel(uint64_t limit_ns) {
+static __global__ void wait_timeout_kernel(uint64_t limit_ns) {
     __shared__ __align__(8) uint64_t bar;
     __shared__ int abort_poll, abort_sleep;
     if (threadIdx.x == 0) {

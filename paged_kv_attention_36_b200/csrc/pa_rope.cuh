@@ -1,0 +1,339 @@
+// pa_rope.cuh -- the step's append with the position rotation on the way:
+// q and k rows are turned by the angles of their tokens' positions, k and v
+// land in their slots of the paged cache (bf16, or 8-bit codes with a scale
+// for each (block, kv head)).
+//
+// A row's first rd values are rd/2 pairs; pair i is (x_i, x_{i+rd/2}), or
+// (x_2i, x_2i+1) when interleaved, and becomes
+//     (a cos_i - b sin_i,  b cos_i + a sin_i)
+// with the angles' cosines and sines read from the caller's fp32 table
+// [max_position][rd] (rd/2 cosines, then rd/2 sines).  Products and sums are
+// single fp32 operations (no contraction), rounded once at the end.
+#pragma once
+
+#include "pa_append.cuh"
+#include "pa_device.cuh"
+
+namespace pa {
+
+struct RopeParams {
+    const __nv_bfloat16* q;       // [T][Hq][D], token stride q_stride (null: no queries)
+    const __nv_bfloat16* k_new;   // [T][Hkv][D], token stride k_stride
+    const __nv_bfloat16* v_new;   // [T][Hkv][D], token stride v_stride
+    int64_t q_stride, k_stride, v_stride;  // in values
+    const int32_t* positions;     // [T]
+    const float* cos_sin;         // [max_position][rd]
+    const int32_t* slot_mapping;  // [T]
+    __nv_bfloat16* q_out;         // [T][Hq][D]
+    void* k_cache;                // bf16 [NB][Hkv][bs][D], or int8 [NB][Hkv][16][D]
+    void* v_cache;                // bf16 [NB][Hkv][bs][D], or int8 [NB][Hkv][D][16]
+    float* k_scale;               // [NB][Hkv] (8-bit)
+    float* v_scale;
+    int32_t T, Hq, Hkv, D, bs, NB;
+    int32_t max_position, rd, interleaved;
+    int32_t kv_ctas;              // 8-bit: the first kv_ctas CTAs take the blocks, the others the queries
+};
+
+constexpr int kRopeThreads = 256;
+
+// (a, b) turned by the angle whose cosine and sine are c and s.
+__device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
+    const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+    b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+    a = x;
+}
+
+// The table row of token t's position (its own row 0, with an error, if the
+// position has none).
+__device__ __forceinline__ const float* angles(const RopeParams& p, int64_t t, bool report) {
+    int32_t pos = __ldg(p.positions + t);
+    if (pos < 0 || pos >= p.max_position) {
+        if (report) raise_error(PA_DEVERR_POSITION);
+        pos = 0;
+    }
+    return p.cos_sin + int64_t(pos) * p.rd;
+}
+
+// 16 values of a row as two 16-byte chunks: the columns of chunk pair c of a
+// row of D values (c < D/16).  Rotated pairs lie within one chunk pair.
+struct ChunkPair {
+    int32_t lo, hi;  // first columns of the two chunks
+    int32_t angle;   // index of the first angle, -1 past the rotated part
+};
+__device__ __forceinline__ ChunkPair chunk_pair(int c, int rd, bool interleaved) {
+    const int n = rd / 16;  // chunk pairs that are rotated
+    if (c >= n) return {16 * c, 16 * c + 8, -1};
+    if (interleaved) return {16 * c, 16 * c + 8, 8 * c};
+    return {8 * c, 8 * c + rd / 2, 8 * c};
+}
+
+// Turns the 16 values of a chunk pair in place (8 angles, cosines cs[0..7], sines cs[rd/2 ..]).
+__device__ __forceinline__ void turn_chunks(uint4& lo, uint4& hi, const float (&c)[8], const float (&s)[8],
+                                            bool interleaved) {
+    uint32_t* w[2] = {&lo.x, &hi.x};
+    float x[16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = bf16x2_to_float2(w[h][j]);
+            x[8 * h + 2 * j] = f.x;
+            x[8 * h + 2 * j + 1] = f.y;
+        }
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], c[i], s[i]);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[h][j] = float2_to_bf16x2(x[8 * h + 2 * j], x[8 * h + 2 * j + 1]);
+}
+
+// Rows [h0, h0 + n) of token t, chunk pair c: heads 0 .. Hq-1 are the
+// queries, then the keys, then the values (bf16 caches).
+__device__ __forceinline__ void rope_rows(const RopeParams& p, int64_t t, int h0, int n, int c) {
+    const int32_t slot = __ldg(p.slot_mapping + t);
+    if (slot < 0) return;  // padding
+    const int64_t block = slot / p.bs, offset = slot - block * p.bs;
+    const bool stored = block < p.NB;
+    if (!stored && c == 0 && h0 == 0) raise_error(PA_DEVERR_SLOT);
+    const ChunkPair cp = chunk_pair(c, p.rd, p.interleaved);
+    float cs[8], sn[8];
+    if (cp.angle >= 0) {
+        const float* a = angles(p, t, c == 0 && h0 == 0) + cp.angle;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(a + i));
+            const float4 y = __ldg(reinterpret_cast<const float4*>(a + p.rd / 2 + i));
+            cs[i] = x.x, cs[i + 1] = x.y, cs[i + 2] = x.z, cs[i + 3] = x.w;
+            sn[i] = y.x, sn[i + 1] = y.y, sn[i + 2] = y.z, sn[i + 3] = y.w;
+        }
+    }
+    for (int h = h0; h < h0 + n; ++h) {
+        const __nv_bfloat16* src;
+        __nv_bfloat16* dst;
+        bool rotate = cp.angle >= 0;
+        if (h < p.Hq) {
+            src = p.q + t * p.q_stride + int64_t(h) * p.D;
+            dst = p.q_out + (t * p.Hq + h) * p.D;
+        } else {
+            if (!stored) continue;
+            const bool v = h >= p.Hq + p.Hkv;
+            const int g = h - p.Hq - (v ? p.Hkv : 0);
+            src = v ? p.v_new + t * p.v_stride + int64_t(g) * p.D : p.k_new + t * p.k_stride + int64_t(g) * p.D;
+            dst = static_cast<__nv_bfloat16*>(v ? p.v_cache : p.k_cache) +
+                  ((block * p.Hkv + g) * p.bs + offset) * p.D;
+            rotate = rotate && !v;
+        }
+        uint4 lo = *reinterpret_cast<const uint4*>(src + cp.lo), hi = *reinterpret_cast<const uint4*>(src + cp.hi);
+        if (rotate) turn_chunks(lo, hi, cs, sn, p.interleaved);
+        *reinterpret_cast<uint4*>(dst + cp.lo) = lo;
+        *reinterpret_cast<uint4*>(dst + cp.hi) = hi;
+    }
+}
+
+// One thread per chunk pair of HP consecutive rows of a token.
+template <int HP>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
+    const int heads = p.Hq + 2 * p.Hkv, groups = (heads + HP - 1) / HP, cpr = p.D / 16;
+    const int64_t i = int64_t(blockIdx.x) * kRopeThreads + threadIdx.x;
+    const int64_t t = i / (groups * cpr);
+    if (t >= p.T) return;
+    const int r = int(i - t * (groups * cpr)), h0 = r / cpr * HP;
+    rope_rows(p, t, h0, heads - h0 < HP ? heads - h0 : HP, r % cpr);
+}
+
+// ---- 8-bit caches ------------------------------------------------------------
+// A block's codes share one scale per kv head, so its new rows are taken
+// together: the CTA of the first token (in call order) whose slot lies in
+// the block writes all of the call's rows of that block, the CTAs of its
+// other tokens leave.  A warp owns one (kv head, K or V) tile at a time.
+// Lane l holds four values of a row (16 lanes cover a row at head_dim 64, so
+// a warp takes two rows at once there), chosen so that a rotated pair never
+// crosses lanes; all 16 rows of its columns stay in registers, so a V row of
+// the transposed tile is one 16-byte (head_dim 64: 8-byte) store.
+//
+//   top = max |x| over the block's new rows,  old = the block's scale (0 if
+//   the call writes the block's row 0: the block starts anew),
+//   scale = max(old, top / 127),  code = round(x / scale);
+//   a larger scale rounds the block's old codes again: round(code old / scale).
+//
+// Division, product and rounding are IEEE fp32 (ties to even).  NaN and
+// infinity go into the scale and poison the block until it starts anew.
+
+// Largest magnitude as bits: non-finite values compare above finite ones, NaN highest.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+__device__ __forceinline__ int quantize(float x, float scale) {
+    if (!(scale > 0.f)) return 0;
+    const int c = __float2int_rn(__fdiv_rn(x, scale));
+    return c > 127 ? 127 : c < -127 ? -127 : c;
+}
+
+template <int D>
+__device__ __forceinline__ void quantize_tile(const RopeParams& p, const int (&src)[16], int64_t block, int g, bool v,
+                                              int lane) {
+    constexpr int LPR = D / 4;        // lanes per row
+    constexpr int NR = 16 * LPR / 32;  // rows a lane holds: 16, or 8 at head_dim 64
+    const int half = lane / LPR, l = lane % LPR;
+    // this lane's four columns: lo, lo+1, hi, hi+1
+    const int rd = v ? 0 : p.rd;
+    int lo = 4 * l, hi = 4 * l + 2;
+    const bool rotate = 4 * l < rd;
+    if (rotate && !p.interleaved) {
+        lo = 2 * l;
+        hi = 2 * l + rd / 2;
+    }
+    // rows in the order of the V tile's bytes: at head_dim 64 the first half
+    // warp has tokens 0-3 and 8-11, the second 4-7 and 12-15
+    auto row_of = [&](int j) -> int { return NR == 16 ? j : (j & 3) + ((j >> 2) << 3) + 4 * half; };
+
+    float x[NR][4];
+    uint32_t top = 0;
+    bool any_old = false;  // rows of the block that the call does not write
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+        const int t = src[row_of(j)];
+        x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
+        if (t < 0) {
+            any_old = true;
+            continue;
+        }
+        const __nv_bfloat16* row = v ? p.v_new + t * p.v_stride + int64_t(g) * D : p.k_new + t * p.k_stride + int64_t(g) * D;
+        const float2 a = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(row + lo));
+        const float2 b = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(row + hi));
+        x[j][0] = a.x;
+        x[j][1] = a.y;
+        x[j][2] = b.x;
+        x[j][3] = b.y;
+        if (rotate) {
+            const float* cs = angles(p, t, false) + 2 * l;
+            const float2 c = __ldg(reinterpret_cast<const float2*>(cs));
+            const float2 s = __ldg(reinterpret_cast<const float2*>(cs + rd / 2));
+            if (p.interleaved) {
+                turn(x[j][0], x[j][1], c.x, s.x);
+                turn(x[j][2], x[j][3], c.y, s.y);
+            } else {
+                turn(x[j][0], x[j][2], c.x, s.x);
+                turn(x[j][1], x[j][3], c.y, s.y);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, abs_bits(x[j][e]));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+
+    const int64_t tile = block * p.Hkv + g;
+    float* scale_at = (v ? p.v_scale : p.k_scale) + tile;
+    const bool anew = src[0] >= 0;
+    const float old = anew ? 0.f : *scale_at;
+    const float need = __fdiv_rn(__uint_as_float(top), 127.f);
+    const float scale = need <= old || old != old ? old : need;  // NaN stays
+    const bool grown = !(scale <= old);
+    __syncwarp();
+    if (lane == 0 && (grown || anew)) *scale_at = scale;
+
+    auto again = [&](int code) -> int {  // an old code under the new scale
+        const int c = scale > 0.f ? __float2int_rn(__fdiv_rn(__fmul_rn(float(code), old), scale)) : 0;
+        return c > 127 ? 127 : c < -127 ? -127 : c;
+    };
+    if (!v) {
+        int8_t* base = static_cast<int8_t*>(p.k_cache) + tile * 16 * D;
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+            const int r = row_of(j);
+            char2* at_lo = reinterpret_cast<char2*>(base + r * D + lo);
+            char2* at_hi = reinterpret_cast<char2*>(base + r * D + hi);
+            if (src[r] >= 0) {
+                *at_lo = make_char2(quantize(x[j][0], scale), quantize(x[j][1], scale));
+                *at_hi = make_char2(quantize(x[j][2], scale), quantize(x[j][3], scale));
+            } else if (anew) {
+                *at_lo = make_char2(0, 0);
+                *at_hi = make_char2(0, 0);
+            } else if (grown) {
+                const char2 a = *at_lo, b = *at_hi;
+                *at_lo = make_char2(again(a.x), again(a.y));
+                *at_hi = make_char2(again(b.x), again(b.y));
+            }
+        }
+    } else {
+        // column d's bytes of the transposed tile: this lane's NR of the 16
+        int8_t* base = static_cast<int8_t*>(p.v_cache) + tile * 16 * D;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            int8_t* at = base + (4 * l + e) * 16 + 8 * half;
+            uint32_t w[NR / 4];
+            if constexpr (NR == 16) {
+                const uint4 o = any_old && !anew ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+                w[0] = o.x, w[1] = o.y, w[2] = o.z, w[3] = o.w;
+            } else {
+                const uint2 o = any_old && !anew ? *reinterpret_cast<const uint2*>(at) : make_uint2(0, 0);
+                w[0] = o.x, w[1] = o.y;
+            }
+#pragma unroll
+            for (int j = 0; j < NR; ++j) {
+                const int r = row_of(j);
+                const int byte = NR == 16 ? 4 * ((j & 7) >> 1) + 2 * (j >> 3) + (j & 1)
+                                          : 4 * ((j & 3) >> 1) + 2 * (j >> 2) + (j & 1);
+                const int sh = 8 * (byte & 3);
+                int code;
+                if (src[r] >= 0) code = quantize(x[j][e], scale);
+                else if (grown) code = again(int8_t(w[byte >> 2] >> sh));
+                else continue;
+                w[byte >> 2] = (w[byte >> 2] & ~(0xffu << sh)) | (uint32_t(code & 0xff) << sh);
+            }
+            if constexpr (NR == 16) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_i8_kernel(const __grid_constant__ RopeParams p) {
+    if (int(blockIdx.x) >= p.kv_ctas) {  // the queries
+        constexpr int cpr = D / 16;
+        const int64_t i = (int64_t(blockIdx.x) - p.kv_ctas) * kRopeThreads + threadIdx.x;
+        const int64_t t = i / (p.Hq * cpr);
+        if (t >= p.T) return;
+        const int r = int(i - t * (p.Hq * cpr));
+        rope_rows(p, t, r / cpr, 1, r % cpr);
+        return;
+    }
+    __shared__ int src[16];    // the call's token of each row of the block, -1: none
+    __shared__ int not_first;  // another token of the block comes before
+    const int t = blockIdx.x;
+    const int32_t slot = __ldg(p.slot_mapping + t);
+    if (slot < 0) return;
+    const int32_t block = slot / 16;
+    if (block >= p.NB) {
+        if (threadIdx.x == 0) raise_error(PA_DEVERR_SLOT);
+        return;
+    }
+    if (p.rd > 0) angles(p, t, threadIdx.x == 0);  // reports a position without a table row
+    if (t > 0) {
+        const int32_t before = __ldg(p.slot_mapping + t - 1);
+        if (before >= 0 && before / 16 == block) return;
+    }
+    if (threadIdx.x < 16) src[threadIdx.x] = -1;
+    if (threadIdx.x == 0) not_first = 0;
+    __syncthreads();
+    for (int u = threadIdx.x; u < p.T; u += kRopeThreads) {
+        const int32_t s = __ldg(p.slot_mapping + u);
+        if (s < 0 || s / 16 != block) continue;
+        if (u < t) not_first = 1;
+        atomicMax(&src[s & 15], u);  // of two tokens in one slot the later lands
+    }
+    __syncthreads();
+    if (not_first) return;
+    int rows[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) rows[r] = src[r];
+    for (int x = threadIdx.x >> 5; x < 2 * p.Hkv; x += kRopeThreads / 32)
+        quantize_tile<D>(p, rows, block, x >> 1, x & 1, threadIdx.x & 31);
+}
+
+}  // namespace pa

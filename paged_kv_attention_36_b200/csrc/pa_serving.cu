@@ -1,0 +1,276 @@
+// pa_serving.cu -- the entry points of include/pa.h for windowed attention,
+// the 8-bit cache with a scale for each (block, kv head), and the append with
+// the position rotation: host-side checks and launches.
+#include "pa_attend_simple.cuh"
+#include "pa_host.cuh"
+#include "pa_rope.cuh"
+
+bool pa::serving_error_word(unsigned int* bits, bool clear) { return read_error_word(bits, clear); }
+
+namespace {
+
+pa_status launched() { return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA; }
+
+struct Call {  // the arguments the attention calls share
+    const void* q;
+    const int32_t* cu_q_lens;
+    int32_t max_q_len;
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    float scale;
+    int32_t window, sinks;
+    void* out;
+    const pa_dims* dims;
+};
+
+bool window_ok(const Call& c) { return c.window >= 1 && c.sinks >= 0; }
+
+pa_status scales_ok(const Call& c) {
+    if (!c.k_scale || !c.v_scale) return PA_ERR_NULL;
+    return aligned4(c.k_scale) && aligned4(c.v_scale) ? PA_OK : PA_ERR_ALIGN;
+}
+
+// Checks of a multi-query call; *done: there is nothing to compute.
+pa_status check_prefill(const Call& c, bool* done) {
+    *done = true;
+    if (!c.dims) return PA_ERR_NULL;
+    if (!dims_ok(c.dims) || c.max_q_len < 0 || !window_ok(c)) return PA_ERR_SHAPE;
+    const pa_dims& d = *c.dims;
+    const int G = d.num_q_heads / d.num_kv_heads;
+    if (d.block_size != kBlockSize || !supported(d.head_dim, G, MathKind::kMma)) return PA_ERR_UNSUPPORTED;
+    if (d.num_seqs == 0 || c.max_q_len == 0) return PA_OK;
+    if (d.num_blocks == 0) return PA_ERR_SHAPE;
+    if (!c.q || !c.cu_q_lens || !c.k_cache || !c.v_cache || !c.block_tables || !c.context_lens || !c.out)
+        return PA_ERR_NULL;
+    if (!aligned16(c.q) || !aligned16(c.out) || !aligned16(c.k_cache) || !aligned16(c.v_cache) ||
+        !aligned4(c.cu_q_lens) || !aligned4(c.block_tables) || !aligned4(c.context_lens))
+        return PA_ERR_ALIGN;
+    if (int64_t(d.num_blocks) * d.num_kv_heads * d.block_size >= (int64_t(1) << 31)) return PA_ERR_SHAPE;
+    const int64_t tiles = (int64_t(c.max_q_len) * G + 127) / 128;
+    if (int64_t(d.num_seqs) * tiles > 0x7fffffffLL || d.num_kv_heads > 65535) return PA_ERR_SHAPE;
+    *done = false;
+    return PA_OK;
+}
+
+template <bool I8>
+pa_status attend_simple(const Call& c, cudaStream_t s) {
+    const pa_dims& d = *c.dims;
+    pa::AttendParams p;
+    p.q = static_cast<const __nv_bfloat16*>(c.q);
+    p.k_cache = c.k_cache;
+    p.v_cache = c.v_cache;
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
+    p.cu_q_lens = c.cu_q_lens;
+    p.block_tables = c.block_tables;
+    p.context_lens = c.context_lens;
+    p.out = static_cast<__nv_bfloat16*>(c.out);
+    p.B = d.num_seqs;
+    p.Hq = d.num_q_heads;
+    p.Hkv = d.num_kv_heads;
+    p.NB = d.num_blocks;
+    p.M = d.max_blocks_per_seq;
+    p.window = c.window;
+    p.sinks = c.sinks;
+    p.qscale = c.scale * kLog2e;
+    const int rows = c.cu_q_lens ? c.max_q_len : 1;
+    const dim3 grid(unsigned(d.num_seqs), unsigned((d.num_q_heads + 3) / 4), unsigned(rows < 1024 ? rows : 1024));
+    if (d.head_dim == 64) pa::attend_simple_kernel<64, I8><<<grid, 128, 0, s>>>(p);
+    else pa::attend_simple_kernel<128, I8><<<grid, 128, 0, s>>>(p);
+    return launched();
+}
+
+struct Append {  // the arguments of an append with rotation
+    const void* q;
+    int64_t q_stride;
+    const void* k_new;
+    int64_t k_stride;
+    const void* v_new;
+    int64_t v_stride;
+    const pa_rope* rope;
+    const int32_t* slot_mapping;
+    int32_t num_tokens;
+    void* q_out;
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;
+    float* v_scale;
+    const pa_dims* dims;
+};
+
+// Checks an append and fills p; p.T = 0: there is nothing to do.
+pa_status prepare_append(const Append& a, bool i8, pa::RopeParams& p) {
+    p = pa::RopeParams{};
+    if (!a.dims) return PA_ERR_NULL;
+    const pa_dims& d = *a.dims;
+    const int rd = a.rope ? a.rope->rotary_dim : 0;
+    if (a.num_tokens < 0 || d.num_kv_heads <= 0 || d.head_dim <= 0 || d.block_size <= 0 || d.num_blocks < 0 ||
+        (a.q && d.num_q_heads <= 0) || rd < 0 || rd > d.head_dim)
+        return PA_ERR_SHAPE;
+    if (d.head_dim % 16 != 0 || rd % 16 != 0) return PA_ERR_UNSUPPORTED;
+    if (i8 && (d.block_size != kBlockSize || (d.head_dim != 64 && d.head_dim != 128))) return PA_ERR_UNSUPPORTED;
+    if (a.num_tokens == 0) return PA_OK;
+    if (!a.k_new || !a.v_new || !a.slot_mapping || !a.k_cache || !a.v_cache || (a.q && !a.q_out) ||
+        (i8 && (!a.k_scale || !a.v_scale)))
+        return PA_ERR_NULL;
+    if (rd > 0) {
+        if (!a.rope->positions || !a.rope->cos_sin) return PA_ERR_NULL;
+        if (a.rope->max_position <= 0) return PA_ERR_SHAPE;
+        if (!aligned4(a.rope->positions) || !aligned16(a.rope->cos_sin)) return PA_ERR_ALIGN;
+    }
+    const int64_t qw = int64_t(d.num_q_heads) * d.head_dim, kw = int64_t(d.num_kv_heads) * d.head_dim;
+    if ((a.q && a.q_stride < qw) || a.k_stride < kw || a.v_stride < kw) return PA_ERR_SHAPE;
+    if ((a.q && a.q_stride % 8) || a.k_stride % 8 || a.v_stride % 8 || (a.q && (!aligned16(a.q) || !aligned16(a.q_out))) ||
+        !aligned16(a.k_new) || !aligned16(a.v_new) || !aligned16(a.k_cache) || !aligned16(a.v_cache) ||
+        !aligned4(a.slot_mapping) || (i8 && (!aligned4(a.k_scale) || !aligned4(a.v_scale))))
+        return PA_ERR_ALIGN;
+    if (a.q && !(a.q == a.q_out && a.q_stride == qw)) {  // in place, or apart: rows written before they are read otherwise
+        const uintptr_t q0 = reinterpret_cast<uintptr_t>(a.q), o0 = reinterpret_cast<uintptr_t>(a.q_out);
+        const uintptr_t q1 = q0 + ((a.num_tokens - 1) * a.q_stride + qw) * 2, o1 = o0 + a.num_tokens * qw * 2;
+        // q's rows may lie between rows of another buffer, q_out's do not
+        if (q0 < o1 && o0 < q1) return PA_ERR_SHAPE;
+    }
+    if (int64_t(d.num_blocks) * d.block_size > 0x7fffffffLL) return PA_ERR_SHAPE;  // slots are int32
+    p.q = static_cast<const __nv_bfloat16*>(a.q);
+    p.k_new = static_cast<const __nv_bfloat16*>(a.k_new);
+    p.v_new = static_cast<const __nv_bfloat16*>(a.v_new);
+    p.q_stride = a.q_stride;
+    p.k_stride = a.k_stride;
+    p.v_stride = a.v_stride;
+    if (rd > 0) {
+        p.positions = a.rope->positions;
+        p.cos_sin = a.rope->cos_sin;
+        p.max_position = a.rope->max_position;
+        p.interleaved = a.rope->interleaved != 0;
+    }
+    p.rd = rd;
+    p.slot_mapping = a.slot_mapping;
+    p.q_out = static_cast<__nv_bfloat16*>(a.q_out);
+    p.k_cache = a.k_cache;
+    p.v_cache = a.v_cache;
+    p.k_scale = a.k_scale;
+    p.v_scale = a.v_scale;
+    p.T = a.num_tokens;
+    p.Hq = a.q ? d.num_q_heads : 0;
+    p.Hkv = d.num_kv_heads;
+    p.D = d.head_dim;
+    p.bs = d.block_size;
+    p.NB = d.num_blocks;
+    return PA_OK;
+}
+
+template <int HP>
+pa_status launch_rope(const pa::RopeParams& p, cudaStream_t s) {
+    const int64_t items = int64_t(p.T) * ((p.Hq + 2 * p.Hkv + HP - 1) / HP) * (p.D / 16);
+    const int64_t ctas = (items + pa::kRopeThreads - 1) / pa::kRopeThreads;
+    if (ctas > 0x7fffffff) return PA_ERR_SHAPE;
+    pa::rope_append_kernel<HP><<<unsigned(ctas), pa::kRopeThreads, 0, s>>>(p);
+    return launched();
+}
+
+pa_status append_i8(const Append& a, cudaStream_t s) {
+    pa::RopeParams p;
+    const pa_status st = prepare_append(a, true, p);
+    if (st != PA_OK || p.T == 0) return st;
+    const int64_t q_items = int64_t(p.T) * p.Hq * (p.D / 16);
+    const int64_t ctas = p.T + (q_items + pa::kRopeThreads - 1) / pa::kRopeThreads;
+    if (ctas > 0x7fffffff) return PA_ERR_SHAPE;
+    p.kv_ctas = p.T;
+    if (p.D == 64) pa::rope_append_i8_kernel<64><<<unsigned(ctas), pa::kRopeThreads, 0, s>>>(p);
+    else pa::rope_append_i8_kernel<128><<<unsigned(ctas), pa::kRopeThreads, 0, s>>>(p);
+    return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_decode_window(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                           const int32_t* context_lens, float scale, int32_t window, int32_t sinks, void* out,
+                           const pa_dims* dims, void* workspace, size_t workspace_bytes, void* stream) {
+    const Call c{q, nullptr, 1, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, scale, window, sinks,
+                 out, dims};
+    if (!dims) return PA_ERR_NULL;
+    if (!window_ok(c)) return PA_ERR_SHAPE;
+    pa::DecodeParams p;
+    const pa_status st = prepare_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out, dims, sm_count(),
+                                        workspace, workspace_bytes, p);
+    if (st != PA_OK || dims->num_seqs == 0) return st;
+    return attend_simple<false>(c, static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_decode_i8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                       const float* v_scale, const int32_t* block_tables, const int32_t* context_lens, float scale,
+                       int32_t window, int32_t sinks, void* out, const pa_dims* dims, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    const Call c{q, nullptr, 1, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, window, sinks,
+                 out, dims};
+    if (!dims) return PA_ERR_NULL;
+    if (!window_ok(c)) return PA_ERR_SHAPE;
+    pa::DecodeParams p;
+    pa_status st = prepare_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out, dims, sm_count(),
+                                  workspace, workspace_bytes, p, /*eb=*/1);
+    if (st != PA_OK || dims->num_seqs == 0) return st;
+    if ((st = scales_ok(c)) != PA_OK) return st;
+    return attend_simple<true>(c, static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_prefill_window(const void* q, const int32_t* cu_q_lens, int32_t max_q_len, const void* k_cache,
+                            const void* v_cache, const int32_t* block_tables, const int32_t* context_lens, float scale,
+                            int32_t window, int32_t sinks, void* out, const pa_dims* dims, void* stream) {
+    const Call c{q, cu_q_lens, max_q_len, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, scale,
+                 window, sinks, out, dims};
+    bool done;
+    const pa_status st = check_prefill(c, &done);
+    if (st != PA_OK || done) return st;
+    return attend_simple<false>(c, static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_len, const void* k_cache,
+                        const void* v_cache, const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                        const int32_t* context_lens, float scale, int32_t window, int32_t sinks, void* out,
+                        const pa_dims* dims, void* stream) {
+    const Call c{q, cu_q_lens, max_q_len, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale,
+                 window, sinks, out, dims};
+    bool done;
+    pa_status st = check_prefill(c, &done);
+    if (st != PA_OK || done) return st;
+    if ((st = scales_ok(c)) != PA_OK) return st;
+    return attend_simple<true>(c, static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                         int64_t v_stride, const pa_rope* rope, const int32_t* slot_mapping, int32_t num_tokens,
+                         void* q_out, void* k_cache, void* v_cache, const pa_dims* dims, void* stream) {
+    pa::RopeParams p;
+    const pa_status st = prepare_append(Append{q, q_stride, k_new, k_stride, v_new, v_stride, rope, slot_mapping,
+                                               num_tokens, q_out, k_cache, v_cache, nullptr, nullptr, dims},
+                                        false, p);
+    if (st != PA_OK || p.T == 0) return st;
+    return launch_rope<1>(p, static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_rope_append_i8(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
+                            int64_t v_stride, const pa_rope* rope, const int32_t* slot_mapping, int32_t num_tokens,
+                            void* q_out, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                            const pa_dims* dims, void* stream) {
+    return append_i8(Append{q, q_stride, k_new, k_stride, v_new, v_stride, rope, slot_mapping, num_tokens, q_out,
+                            k_cache, v_cache, k_scale, v_scale, dims},
+                     static_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_cache_append_i8(const void* k_new, const void* v_new, const int32_t* slot_mapping, int32_t num_tokens,
+                             void* k_cache, void* v_cache, float* k_scale, float* v_scale, const pa_dims* dims,
+                             void* stream) {
+    if (!dims) return PA_ERR_NULL;
+    const int64_t w = int64_t(dims->num_kv_heads) * dims->head_dim;
+    return append_i8(Append{nullptr, 0, k_new, w, v_new, w, nullptr, slot_mapping, num_tokens, nullptr, k_cache,
+                            v_cache, k_scale, v_scale, dims},
+                     static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
