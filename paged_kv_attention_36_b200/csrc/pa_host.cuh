@@ -228,12 +228,13 @@ bool make_fp8_map(CUtensorMap* map, const void* base, int64_t tiles, int D, int 
 // Shared validation of the decode calls; fills p.
 pa_status prepare_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                          const int32_t* context_lens, float scale, void* out, const pa_dims* dims, int grid,
-                         void* workspace, size_t workspace_bytes, pa::DecodeParams& p, int eb = 2) {
+                         void* workspace, size_t workspace_bytes, pa::DecodeParams& p, int eb = 2,
+                         MathKind mk = math_kind()) {
     if (!dims) return PA_ERR_NULL;
     if (!dims_ok(dims)) return PA_ERR_SHAPE;
     const pa_dims& d = *dims;
     const int G = d.num_q_heads / d.num_kv_heads;
-    if (d.block_size != kBlockSize || !supported(d.head_dim, G, eb == 1 ? MathKind::kFp8 : math_kind()))
+    if (d.block_size != kBlockSize || !supported(d.head_dim, G, eb == 1 ? MathKind::kFp8 : mk))
         return PA_ERR_UNSUPPORTED;
     if (d.num_seqs == 0) return PA_OK;
     // at least one block, so that a bad block id can be redirected to block 0

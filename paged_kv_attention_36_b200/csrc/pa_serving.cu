@@ -1,6 +1,8 @@
 // pa_serving.cu -- the entry points of include/pa.h for windowed attention,
 // the 8-bit cache with a scale for each (block, kv head), and the append with
 // the position rotation: host-side checks and launches.
+#include <type_traits>
+
 #include "pa_attend_simple.cuh"
 #include "pa_host.cuh"
 #include "pa_rope.cuh"
@@ -27,7 +29,7 @@ struct Call {  // the arguments the attention calls share
     const pa_dims* dims;
 };
 
-bool window_ok(const Call& c) { return c.window >= 1 && c.sinks >= 0; }
+bool window_ok(int32_t window, int32_t sinks) { return window >= 1 && sinks >= 0; }
 
 pa_status scales_ok(const Call& c) {
     if (!c.k_scale || !c.v_scale) return PA_ERR_NULL;
@@ -38,7 +40,7 @@ pa_status scales_ok(const Call& c) {
 pa_status check_prefill(const Call& c, bool* done) {
     *done = true;
     if (!c.dims) return PA_ERR_NULL;
-    if (!dims_ok(c.dims) || c.max_q_len < 0 || !window_ok(c)) return PA_ERR_SHAPE;
+    if (!dims_ok(c.dims) || c.max_q_len < 0 || !window_ok(c.window, c.sinks)) return PA_ERR_SHAPE;
     const pa_dims& d = *c.dims;
     const int G = d.num_q_heads / d.num_kv_heads;
     if (d.block_size != kBlockSize || !supported(d.head_dim, G, MathKind::kMma)) return PA_ERR_UNSUPPORTED;
@@ -83,6 +85,39 @@ pa_status attend_simple(const Call& c, cudaStream_t s) {
     else pa::attend_simple_kernel<128, I8><<<grid, 128, 0, s>>>(p);
     return launched();
 }
+
+// fn<D, G>() for the head_dim and GQA group of a call that supported() let through.
+template <class F>
+pa_status by_shape(const pa_dims& d, F fn) {
+    const int G = d.num_q_heads / d.num_kv_heads;
+    auto with = [&](auto dim) -> pa_status {
+        constexpr int D = decltype(dim)::value;
+        switch (G) {
+            case 1: return fn.template operator()<D, 1>();
+            case 2: return fn.template operator()<D, 2>();
+            case 4: return fn.template operator()<D, 4>();
+            case 8: return fn.template operator()<D, 8>();
+        }
+        return PA_ERR_UNSUPPORTED;
+    };
+    return d.head_dim == 64 ? with(std::integral_constant<int, 64>{}) : with(std::integral_constant<int, 128>{});
+}
+
+struct DecodeWindow {
+    const pa::DecodeParams& p;
+    int grid;
+    cudaStream_t stream;
+    template <int D, int G>
+    pa_status operator()() const {
+        constexpr int R = ring_fit<D>();
+        using Cfg = pa::DecodeCfg<D, kBlockSize, R>;
+        auto kern = pa::decode_kernel<D, G, kBlockSize, R, false, false, pa::MmaMath, true>;
+        static unsigned attr_done[kMaxDevices];
+        if (!set_smem_once(kern, Cfg::kBaseBytes, attr_done)) return PA_ERR_CUDA;
+        kern<<<grid, Cfg::kThreads, Cfg::kBaseBytes, stream>>>(p);
+        return launched();
+    }
+};
 
 struct Append {  // the arguments of an append with rotation
     const void* q;
@@ -192,15 +227,16 @@ extern "C" {
 pa_status pa_decode_window(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                            const int32_t* context_lens, float scale, int32_t window, int32_t sinks, void* out,
                            const pa_dims* dims, void* workspace, size_t workspace_bytes, void* stream) {
-    const Call c{q, nullptr, 1, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, scale, window, sinks,
-                 out, dims};
     if (!dims) return PA_ERR_NULL;
-    if (!window_ok(c)) return PA_ERR_SHAPE;
+    if (!window_ok(window, sinks)) return PA_ERR_SHAPE;
     pa::DecodeParams p;
-    const pa_status st = prepare_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out, dims, sm_count(),
-                                        workspace, workspace_bytes, p);
+    const int grid = sm_count();
+    const pa_status st = prepare_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out, dims, grid,
+                                        workspace, workspace_bytes, p, /*eb=*/2, MathKind::kMma);
     if (st != PA_OK || dims->num_seqs == 0) return st;
-    return attend_simple<false>(c, static_cast<cudaStream_t>(stream));
+    p.window = window;
+    p.sinks = sinks;
+    return by_shape(*dims, DecodeWindow{p, grid, static_cast<cudaStream_t>(stream)});
 }
 
 pa_status pa_decode_i8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -210,7 +246,7 @@ pa_status pa_decode_i8(const void* q, const void* k_cache, const void* v_cache, 
     const Call c{q, nullptr, 1, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, window, sinks,
                  out, dims};
     if (!dims) return PA_ERR_NULL;
-    if (!window_ok(c)) return PA_ERR_SHAPE;
+    if (!window_ok(c.window, c.sinks)) return PA_ERR_SHAPE;
     pa::DecodeParams p;
     pa_status st = prepare_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out, dims, sm_count(),
                                   workspace, workspace_bytes, p, /*eb=*/1);
