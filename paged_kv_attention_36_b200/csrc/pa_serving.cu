@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "pa_attend_simple.cuh"
+#include "pa_decode_wide.cuh"
 #include "pa_host.cuh"
 #include "pa_rope.cuh"
 
@@ -101,6 +102,86 @@ pa_status by_shape(const pa_dims& d, F fn) {
         return PA_ERR_UNSUPPORTED;
     };
     return d.head_dim == 64 ? with(std::integral_constant<int, 64>{}) : with(std::integral_constant<int, 128>{});
+}
+
+// Launches with programmatic serialization: the kernel's set-up may overlap
+// the end of the one before it (it waits with griddepcontrol.wait).
+template <class Kernel, class Params>
+pa_status launch_dependent(Kernel kern, dim3 grid, int threads, int smem, cudaStream_t stream, const Params& p) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return PA_ERR_CUDA;
+    return launched();
+}
+
+// ---- wide decode ---------------------------------------------------------------
+constexpr int kWideStageK = 8192;      // K bytes of a ring stage, at most
+constexpr int kWideMinBytes = 65536;   // K+V bytes worth a CTA of their own
+constexpr int kMaxSmem = 232448;
+
+int floor_log2(int x) {
+    int n = 0;
+    while (x >> (n + 1)) ++n;
+    return n;
+}
+
+// The ring and the warps for p's head layout; false if it cannot be (no supported layout).
+bool wide_shape(const pa::DecodeParams& p, int D, int eb, pa::WideShape& s) {
+    const int tile = kBlockSize * D * eb;
+    s.HG = p.HG;
+    s.HS = p.HS;
+    s.SPL_LOG = p.SPL_LOG;
+    s.WPH_LOG = floor_log2(pa::kWideWarps / p.HG);
+    s.stage_k = p.HS * tile;
+    const int step = 1 << (s.SPL_LOG + s.WPH_LOG);
+    for (s.R = pa::kWideMaxRing / step * step; s.R > 0; s.R -= step)
+        if (pa::wide_layout(s, D).total + 1024 <= kMaxSmem) break;
+    s.smem = pa::wide_layout(s, D).total + 1024;
+    return s.R > 0;
+}
+
+template <bool I8>
+struct DecodeWide {
+    pa::WideParams& p;
+    int grid;
+    cudaStream_t stream;
+    template <int D, int G>
+    pa_status operator()() const {
+        using MathT = std::conditional_t<I8, pa::I8Math<D, G>, pa::MmaMath<D, G, kBlockSize>>;
+        auto kern = pa::decode_wide_kernel<MathT, D, G, I8>;
+        static unsigned attr_done[kMaxDevices];
+        if (!set_smem_once(kern, kMaxSmem, attr_done)) return PA_ERR_CUDA;
+        if (!wide_shape(p.d, D, I8 ? 1 : 2, p.shape)) return PA_ERR_UNSUPPORTED;
+        const int page = 2 * kBlockSize * D * (I8 ? 1 : 2) * p.d.HG;
+        p.d.min_pages = kWideMinBytes / page > 2 ? kWideMinBytes / page : 2;
+        p.shape.snap = p.d.min_pages / 2;
+        return launch_dependent(kern, dim3(unsigned(grid)), pa::kWideThreads, p.shape.smem, stream, p);
+    }
+};
+
+template <bool I8>
+pa_status decode_wide(const Call& c, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!c.dims) return PA_ERR_NULL;
+    if (!window_ok(c.window, c.sinks)) return PA_ERR_SHAPE;
+    pa::WideParams p;
+    const int grid = sm_count();
+    pa_status st = prepare_decode(c.q, c.k_cache, c.v_cache, c.block_tables, c.context_lens, c.scale, c.out, c.dims,
+                                  grid, workspace, workspace_bytes, p.d, I8 ? 1 : 2, MathKind::kMma, kWideStageK);
+    if (st != PA_OK || c.dims->num_seqs == 0) return st;
+    if (I8 && (st = scales_ok(c)) != PA_OK) return st;
+    p.d.k_scale = c.k_scale;
+    p.d.v_scale = c.v_scale;
+    p.window = c.window;
+    p.sinks = c.sinks;
+    return by_shape(*c.dims, DecodeWide<I8>{p, grid, static_cast<cudaStream_t>(stream)});
 }
 
 struct DecodeWindow {
@@ -245,14 +326,7 @@ pa_status pa_decode_i8(const void* q, const void* k_cache, const void* v_cache, 
                        size_t workspace_bytes, void* stream) {
     const Call c{q, nullptr, 1, k_cache, v_cache, k_scale, v_scale, block_tables, context_lens, scale, window, sinks,
                  out, dims};
-    if (!dims) return PA_ERR_NULL;
-    if (!window_ok(c.window, c.sinks)) return PA_ERR_SHAPE;
-    pa::DecodeParams p;
-    pa_status st = prepare_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out, dims, sm_count(),
-                                  workspace, workspace_bytes, p, /*eb=*/1);
-    if (st != PA_OK || dims->num_seqs == 0) return st;
-    if ((st = scales_ok(c)) != PA_OK) return st;
-    return attend_simple<true>(c, static_cast<cudaStream_t>(stream));
+    return decode_wide<true>(c, workspace, workspace_bytes, stream);
 }
 
 pa_status pa_prefill_window(const void* q, const int32_t* cu_q_lens, int32_t max_q_len, const void* k_cache,
