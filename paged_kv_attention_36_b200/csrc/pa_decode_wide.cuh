@@ -19,15 +19,49 @@
 //   * Share boundaries that would cut fewer than `snap` pages off a segment
 //     move to the segment's end (cut_page): short contexts stay whole, so a
 //     small batch needs no merge between CTAs.
-//   * A page of an 8-bit cache brings its heads' scales along: 4-byte
+//   * A page of an 8-bit cache brings its heads' scales along: two bulk
+//     copies where they are 16-byte pieces (kv heads in fours), else 4-byte
 //     cp.async copies that arrive on the stage's barrier.
 //   * Launched as a programmatic dependent: the set-up overlaps the end of
 //     the kernel before it.
 #pragma once
 
 #include "pa_decode.cuh"
+#include "pa_tcgen05.cuh"
 
 namespace pa {
+
+// ldmatrix and mma forms of this file: shared-memory addresses as they are,
+// and a product without an accumulator to start from.
+__device__ __forceinline__ void ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+// Integer products on the tensor cores: c[16x8 s32] = a[16x32 s8, row-major] *
+// b[32x8, col-major] + c0, b signed or unsigned.
+template <bool B_UNSIGNED>
+__device__ __forceinline__ void imma_16832(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                           const int (&c0)[4]) {
+    if constexpr (B_UNSIGNED)
+        asm volatile(
+            "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c0[0]), "r"(c0[1]), "r"(c0[2]),
+              "r"(c0[3]));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c0[0]), "r"(c0[1]), "r"(c0[2]),
+              "r"(c0[3]));
+}
+// An integer accumulator that starts at these bits reads as the float
+// 12582912 + n while |n| < 2^22, so a subtraction converts it.
+constexpr int kIntBase = 0x4B400000;
+constexpr float kIntBaseF = 12582912.f;
 
 // Page at which a share boundary at line position t cuts a segment of np
 // pages that starts at u0: 0 or np where fewer than `snap` pages (or half
@@ -40,63 +74,41 @@ __host__ __device__ __forceinline__ int32_t cut_page(int64_t t, int64_t u0, int3
 }
 
 // ---- page math over 8-bit codes ------------------------------------------------
-// The tiles are the fp8 policy's (K [16][D] in 128-byte swizzled lines, V
-// transposed in its token order), so the fragments are too: plain ldmatrix
-// gives a lane four consecutive codes of a row.  A code b becomes an f16 by
-// its bytes alone: 0x6400 | (b ^ 0x80) is 1024 + 128 + b.  For K the 1152 is
-// taken back at once for the whole dot product (the accumulator starts at
-// -1152 sum(q)); for V, whose sums are long, value by value (exact).  Queries
-// are scaled by a power of two to at most 2 in f16, which loses nothing
-// bf16 holds down to 2^-14 of the row's largest value; P goes into the second
-// product as f16 (2^-11).  Each page's P V is scaled by the page's V scale
-// when it is added to the fp32 state.
+// Both products run on the integer tensor cores, so no code is ever
+// converted: the tiles (K [16][D], V transposed in its token order) are A
+// operands of mma.sync m16n8k32 as ldmatrix delivers them.  (Converting them
+// to f16 took 24 of the 48 ALU instructions of a 64-wide page and twice the
+// mma; m16n8k32 s8 issues at the rate of m16n8k16 f16 here.)  The other
+// operand is fixed point in 16 bits, as two 8-bit halves:
+//
+//   q = qmax / 32512 * (256 hi + lo), hi and lo signed: off by at most 2^-16
+//     of the row's largest value.  S = 256 (K hi) + K lo, exact in integers.
+//   P: for the 32 tokens of a page pair, y = logit + log2(v_scale) and its
+//     maximum over the pair; w = 2^(y - max) = (256 hi + lo) / 65535, hi and
+//     lo unsigned.  A token's weight is off by at most 2^-17 of the heaviest
+//     contribution of its own pair, whatever the other pairs' weights or the
+//     other blocks' scales are.
+//
+// With up to four heads the halves share an mma: columns 0-3 take the high
+// halves of the heads, columns 4-7 the low ones; both sums of a head meet
+// with one shuffle (S in every page, O once at the end).  With eight heads
+// each half has an mma of its own.  Sums of a pair stay below 2^22 and become
+// fp32 by one subtraction (kIntBase); the state (m, l, O) is fp32.  l comes
+// from the same w, unrounded: 2^(logit - m) = w * 2^(max - m - log2(v_scale)).
+// m follows the pair maxima lazily (raised when one passes it by 15).
 template <int D, int G>
 struct I8Math : MmaMath<D, G, 16> {
     using Base = MmaMath<D, G, 16>;
     using Base::KS;
-    using Base::qb;
     using Base::acc;
     using Base::m;
     using Base::l;
     static constexpr int kElemBytes = 1;
-    float qs[2];    // scale * log2(e) * the query's power of two, heads h0 and h0 + 1
-    float bias[2];  // -1152 * sum of the query's f16 values
-
-    __device__ __forceinline__ void load_q_global(const uint8_t* gq, int lane, float qscale) {
-        const int h = lane >> 2, c = lane & 3;
-        uint2 w[KS];
-        float top = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            w[ks] = h < G ? __ldg(reinterpret_cast<const uint2*>(gq + (h * D + 16 * ks + 4 * c) * 2)) : make_uint2(0, 0);
-            const float2 a = bf16x2_to_float2(w[ks].x), b = bf16x2_to_float2(w[ks].y);
-            top = fmaxf(fmaxf(top, fmaxf(fabsf(a.x), fabsf(a.y))), fmaxf(fabsf(b.x), fabsf(b.y)));
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 0;
-        const float down = exp2f(float(-e));
-        float sum = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            const float2 a = bf16x2_to_float2(w[ks].x), b = bf16x2_to_float2(w[ks].y);
-            qb[ks][0] = float2_to_f16x2(a.x * down, a.y * down);
-            qb[ks][1] = float2_to_f16x2(b.x * down, b.y * down);
-            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&qb[ks][0]));
-            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&qb[ks][1]));
-            sum += (x.x + x.y) + (y.x + y.y);
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const float up = qscale * exp2f(float(e));
-        // a lane's logits are heads h0, h0 + 1, whose rows lanes 4 h0 .. hold
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int from = 4 * (2 * c + i);
-            qs[i] = __shfl_sync(0xffffffffu, up, from);
-            bias[i] = -1152.f * __shfl_sync(0xffffffffu, sum, from);
-        }
-    }
+    static constexpr bool kShared = G <= 4;  // high and low halves share an mma
+    static constexpr int NQ = kShared ? 1 : 2;
+    uint32_t qi[NQ][D / 32][2];  // q's halves as B fragments
+    float qs[2];                 // scale * log2(e) * qmax / 32512 of this lane's two heads
+    uint32_t koff[D / 32];       // this lane's K row, for each 32 columns
 
     // Byte offset of 16-byte chunk ch (d 16ch .. 16ch+15) of token t in a K tile.
     static __device__ __forceinline__ int k_off(int t, int ch) {
@@ -104,81 +116,151 @@ struct I8Math : MmaMath<D, G, 16> {
         const int lch = D == 128 ? ch : (((t & 1) << 2) + ch);
         return (line << 7) + ((lch ^ (line & 7)) << 4);
     }
-    // Codes (0, 1) and (2, 3) of four, plus 1152, as f16 pairs.
-    static __device__ __forceinline__ void biased(uint32_t r, uint32_t& lo, uint32_t& hi) {
-        r ^= 0x80808080u;
-        lo = __byte_perm(r, 0x64646464u, 0x4140);
-        hi = __byte_perm(r, 0x64646464u, 0x4342);
-    }
-    static __device__ __forceinline__ void codes(uint32_t r, uint32_t& lo, uint32_t& hi) {
-        biased(r, lo, hi);
-        const __half2 b = __floats2half2_rn(1152.f, 1152.f);
-        __half2 x = __hsub2(*reinterpret_cast<__half2*>(&lo), b), y = __hsub2(*reinterpret_cast<__half2*>(&hi), b);
-        lo = *reinterpret_cast<uint32_t*>(&x);
-        hi = *reinterpret_cast<uint32_t*>(&y);
+
+    __device__ __forceinline__ void load_q_global(const uint8_t* gq, int lane, float qscale) {
+        const int n = lane >> 2, c = lane & 3;  // this lane's column of the mma
+        const int h = kShared ? n & 3 : n;
+        uint2 w[D / 32][2];
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                w[j][i] = h < G ? __ldg(reinterpret_cast<const uint2*>(gq + (h * D + 32 * j + 16 * i + 4 * c) * 2))
+                                : make_uint2(0u, 0u);
+                const float2 x = bf16x2_to_float2(w[j][i].x), y = bf16x2_to_float2(w[j][i].y);
+                top = fmaxf(fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(y.x), fabsf(y.y)));
+            }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 x = bf16x2_to_float2(w[j][i].x), y = bf16x2_to_float2(w[j][i].y);
+                const float v[4] = {x.x, x.y, y.x, y.y};
+                uint32_t hi = 0, lo = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // v / top first: the quotient is at most 1 however large or small q is
+                    const int q16 = top > 0.f ? __float2int_rn(v[e] / top * 32512.f) : 0;
+                    const int up = (q16 + 128) >> 8;
+                    hi |= uint32_t(up & 0xff) << (8 * e);
+                    lo |= uint32_t((q16 - (up << 8)) & 0xff) << (8 * e);
+                }
+                if constexpr (kShared) {
+                    qi[0][j][i] = n < 4 ? hi : lo;
+                } else {
+                    qi[0][j][i] = hi;
+                    qi[NQ - 1][j][i] = lo;
+                }
+            }
+        // columns 2c and 2c + 1 of S are this lane's; their rows lie in lanes 4 n ..
+        const float unit = qscale * (top / 32512.f);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) qs[i] = __shfl_sync(0xffffffffu, unit, 4 * (2 * c + i));
+        const int mi = lane >> 3, t = (lane & 7) + ((mi & 1) << 3);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) koff[j] = uint32_t(k_off(t, 2 * j + (mi >> 1)));
     }
 
-    __device__ __forceinline__ void page(const uint8_t* kt, const uint8_t* vt, uint32_t vis, float ks, float vs,
-                                         int lane) {
-        const int mi = lane >> 3, r8 = lane & 7;
-        // ---- S^T = K . Q^T ----
-        float s[4] = {bias[0], bias[1], bias[0], bias[1]};
-        {
-            const int t = r8 + ((mi & 1) << 3);
+    // Two pages (shared-memory addresses of their K and V tiles), the tokens
+    // of `vis` counting (0: the page is not there; its addresses are valid).
+    __device__ __forceinline__ void pages(const uint32_t (&kt)[2], const uint32_t (&vt)[2], const uint32_t (&vis)[2],
+                                          const float (&ks)[2], const float (&vs)[2], int lane) {
+        constexpr int base[4] = {kIntBase, kIntBase, kIntBase, kIntBase};
+        const bool high = (lane & 3) < 2;  // (kShared) this lane's columns are high halves
+        const float wt = kShared && !high ? 1.f : 256.f;
+        // ---- y = scale * K . q + log2(v_scale) ----
+        float y[2][4], lv[2];
 #pragma unroll
-            for (int j = 0; j < KS / 2; ++j) {
-                uint32_t r[4], a0[4], a1[4];
-                ldmatrix_x4(r, kt + k_off(t, 2 * j + (mi >> 1)));
-                biased(r[0], a0[0], a0[2]);
-                biased(r[1], a0[1], a0[3]);
-                biased(r[2], a1[0], a1[2]);
-                biased(r[3], a1[1], a1[3]);
-                mma_f16_16816(s, a0, qb[2 * j][0], qb[2 * j][1]);
-                mma_f16_16816(s, a1, qb[2 * j + 1][0], qb[2 * j + 1][1]);
+        for (int i = 0; i < 2; ++i) {
+            int s[NQ][4];
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+                uint32_t a[4];
+                ldsm_x4(a, kt[i] + koff[j]);
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) {
+                    if (j == 0) imma_16832<false>(s[x], a, qi[x][j][0], qi[x][j][1], base);
+                    else imma_16832<false>(s[x], a, qi[x][j][0], qi[x][j][1], s[x]);
+                }
+            }
+            lv[i] = fmaxf(__log2f(vs[i]), -100.f);  // a scale of 0: codes of 0, weight still in l
+            const float c[2] = {qs[0] * ks[i], qs[1] * ks[i]};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float v = fmaf(__int_as_float(s[0][e]), wt, -kIntBaseF * wt);
+                if constexpr (kShared) v += __shfl_xor_sync(0xffffffffu, v, 2);
+                else v += __int_as_float(s[NQ - 1][e]) - kIntBaseF;
+                y[i][e] = fmaf(v, c[e & 1], lv[i]);
+            }
+            if (vis[i] != 0xffffu) {
+                const int t0 = lane >> 2;
+                if (!((vis[i] >> t0) & 1)) y[i][0] = y[i][1] = -INFINITY;
+                if (!((vis[i] >> (t0 + 8)) & 1)) y[i][2] = y[i][3] = -INFINITY;
             }
         }
-        const int t0 = lane >> 2;
-        const bool v0 = (vis >> t0) & 1, v1 = (vis >> (t0 + 8)) & 1;
-        const float c0 = qs[0] * ks, c1 = qs[1] * ks;
-        s[0] = v0 ? s[0] * c0 : -INFINITY;
-        s[1] = v0 ? s[1] * c1 : -INFINITY;
-        s[2] = v1 ? s[2] * c0 : -INFINITY;
-        s[3] = v1 ? s[3] * c1 : -INFINITY;
-        // ---- online softmax over the 16 tokens of each head column ----
-        float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
+        // ---- the pair's maximum of each head column, and the running one ----
+        float b0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
+        float b1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+            b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, off));
+            b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, off));
         }
-        if (__any_sync(0xffffffffu, mx0 > m[0] || mx1 > m[1])) {
-            const float n0 = fmaxf(m[0], mx0), n1 = fmaxf(m[1], mx1);
-            this->rescale(exp2f(m[0] - n0), exp2f(m[1] - n1));
+        if (__any_sync(0xffffffffu, b0 > m[0] + 15.f || b1 > m[1] + 15.f)) {
+            const float n0 = fmaxf(m[0], b0), n1 = fmaxf(m[1], b1);
+            rescale(ex2_approx(m[0] - n0), ex2_approx(m[1] - n1));
             m[0] = n0;
             m[1] = n1;
         }
-        const float p0 = exp2f(s[0] - m[0]), p1 = exp2f(s[1] - m[1]);
-        const float p2 = exp2f(s[2] - m[0]), p3 = exp2f(s[3] - m[1]);
-        l[0] += p0 + p2;
-        l[1] += p1 + p3;
-        // ---- O^T += v_scale * V^T . P^T, two m-tiles (32 rows of V^T) per ldmatrix ----
-        const uint32_t b0 = movmatrix_trans(float2_to_f16x2(p0, p1));
-        const uint32_t b1 = movmatrix_trans(float2_to_f16x2(p2, p3));
+        // ---- weights; l; the 16-bit weights as B fragments ----
+        uint32_t pb[NQ][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float w0 = ex2_approx(y[i][0] - b0), w1 = ex2_approx(y[i][1] - b1);
+            const float w2 = ex2_approx(y[i][2] - b0), w3 = ex2_approx(y[i][3] - b1);
+            l[0] = fmaf(w0 + w2, ex2_approx(b0 - m[0] - lv[i]), l[0]);
+            l[1] = fmaf(w1 + w3, ex2_approx(b1 - m[1] - lv[i]), l[1]);
+            // 2^23 + rint(65535 w): the integer is in the low 16 bits
+            auto fix = [](float w) { return __float_as_uint(fmaf(w, 65535.f, 8388608.f)); };
+            const uint32_t t0 = movmatrix_trans(__byte_perm(fix(w0), fix(w1), 0x5410));  // tokens 2c, 2c+1
+            const uint32_t t8 = movmatrix_trans(__byte_perm(fix(w2), fix(w3), 0x5410));  // tokens 2c+8, 2c+9
+            // one byte of each, in the V rows' token order
+            if constexpr (kShared) {
+                pb[0][i] = __byte_perm(t0, t8, lane < 16 ? 0x7531 : 0x6420);
+            } else {
+                pb[0][i] = __byte_perm(t0, t8, 0x7531);
+                pb[NQ - 1][i] = __byte_perm(t0, t8, 0x6420);
+            }
+        }
+        // ---- O^T += V^T . P^T, two m-tiles (32 rows of V^T) per ldmatrix ----
+        const float f0 = ex2_approx(b0 - m[0]) * (1.f / 65535.f) * wt;
+        const float f1 = ex2_approx(b1 - m[1]) * (1.f / 65535.f) * wt;
+        const uint64_t f2 = f2_pack(f0, f1), down = f2_pack(-kIntBaseF, -kIntBaseF);
 #pragma unroll
         for (int j = 0; j < KS / 2; ++j) {
-            uint32_t r[4], a0[4], a1[4];
-            ldmatrix_x4(r, vt + (32 * j + lane) * 16);
-            codes(r[0], a0[0], a0[2]);
-            codes(r[1], a0[1], a0[3]);
-            codes(r[2], a1[0], a1[2]);
-            codes(r[3], a1[1], a1[3]);
-            float o0[4] = {0.f, 0.f, 0.f, 0.f}, o1[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16_16816(o0, a0, b0, b1);
-            mma_f16_16816(o1, a1, b0, b1);
+            uint32_t r0[4], r1[4];
+            ldsm_x4(r0, vt[0] + uint32_t((32 * j + lane) * 16));
+            ldsm_x4(r1, vt[1] + uint32_t((32 * j + lane) * 16));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[2 * j][i] += vs * o0[i];
-                acc[2 * j + 1][i] += vs * o1[i];
+            for (int t = 0; t < 2; ++t) {
+                const uint32_t a[4] = {r0[2 * t], r0[2 * t + 1], r1[2 * t], r1[2 * t + 1]};
+                int o[NQ][4];
+#pragma unroll
+                for (int x = 0; x < NQ; ++x) imma_16832<true>(o[x], a, pb[x][0], pb[x][1], base);
+                float* dst = acc[2 * j + t];
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    uint64_t v = f2_add(f2_pack(__int_as_float(o[0][e]), __int_as_float(o[0][e + 1])), down);
+                    if constexpr (!kShared) {  // 256 high + low, in units of the high half's factor
+                        const uint64_t w =
+                            f2_add(f2_pack(__int_as_float(o[NQ - 1][e]), __int_as_float(o[NQ - 1][e + 1])), down);
+                        v = f2_fma(w, f2_pack(1.f / 256.f, 1.f / 256.f), v);
+                    }
+                    f2_unpack(f2_fma(v, f2, f2_pack(dst[e], dst[e + 1])), dst[e], dst[e + 1]);
+                }
             }
         }
     }
@@ -194,10 +276,23 @@ struct I8Math : MmaMath<D, G, 16> {
             acc[i][3] *= a1;
         }
     }
+
+    // The high and the low halves' sums of each head meet (before finish()).
+    __device__ __forceinline__ void join_halves() {
+        if constexpr (kShared) {
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][e] += __shfl_xor_sync(0xffffffffu, acc[i][e], 2);
+        }
+    }
 };
 
 // ---- shared memory ---------------------------------------------------------------
-constexpr int kWideWarps = 16;  // consumer warps
+#ifndef PA_WIDE_WARPS
+#define PA_WIDE_WARPS 8
+#endif
+constexpr int kWideWarps = PA_WIDE_WARPS;  // consumer warps
 constexpr int kWideThreads = (kWideWarps + 1) * 32;
 constexpr int kWideSegs = 4;    // segment descriptors in flight
 constexpr int kWideMaxRing = 32;
@@ -237,6 +332,175 @@ __host__ __device__ inline WideLayout wide_layout(const WideShape& s, int D) {
     w.misc = w.bars + (2 * s.R + 2 * kWideSegs + 2 * s.HG) * 8;
     w.total = w.misc + ((int(sizeof(WideMisc)) + 15) & ~15);
     return w;
+}
+
+// ---- pieces of a (b, kv head) that share boundaries cut --------------------------
+// A piece's state goes to its partial slot as it lies in the fragments,
+// unnormalised: float4 (16-row tile mt, row d0, head pair c) at
+// (8 mt + d0) * G/2 + c holds (h, d), (h+1, d), (h, d+8), (h+1, d+8) with
+// h = 2c, d = 16 mt + d0, and ml[c] = (m_h, m_h+1, l_h, l_h+1); with one head
+// the pairs (d, d+8) are float2 and ml is (m, l).  The same bytes as [G][D]
+// floats, written and read 16 at a time.
+template <int G>
+struct RawPiece {
+    static constexpr int GP = G > 1 ? G / 2 : 1;
+    // After finish(): this warp's state to o, ml.
+    template <class M>
+    static __device__ __forceinline__ void store(const M& st, float* o, float2* ml, int lane) {
+        const int c = lane & 3, d0 = lane >> 2;
+        if (c >= GP) return;
+#pragma unroll
+        for (int mt = 0; mt < M::KS; ++mt) {
+            if constexpr (G > 1)
+                reinterpret_cast<float4*>(o)[(8 * mt + d0) * GP + c] =
+                    make_float4(st.acc[mt][0], st.acc[mt][1], st.acc[mt][2], st.acc[mt][3]);
+            else
+                reinterpret_cast<float2*>(o)[8 * mt + d0] = make_float2(st.acc[mt][0], st.acc[mt][2]);
+        }
+        if (d0 == 0) {
+            if constexpr (G > 1)
+                reinterpret_cast<float4*>(ml)[c] = make_float4(st.m[0], st.m[1], st.l[0], st.l[1]);
+            else
+                ml[0] = make_float2(st.m[0], st.l[0]);
+        }
+    }
+    // After finish(): folds the stored piece (the one before this state in
+    // page order iff before) into the state; the same bits whichever of the
+    // two was stored.
+    template <class M>
+    static __device__ __forceinline__ void fold(M& st, const float* o, const float2* ml, bool before, int lane) {
+        const int c = lane & 3, d0 = lane >> 2;
+        if (c >= GP) return;
+        float4 v[M::KS], w;
+#pragma unroll
+        for (int mt = 0; mt < M::KS; ++mt) {
+            if constexpr (G > 1) {
+                v[mt] = __ldcg(reinterpret_cast<const float4*>(o) + (8 * mt + d0) * GP + c);
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(o) + 8 * mt + d0);
+                v[mt] = make_float4(x.x, 0.f, x.y, 0.f);
+            }
+        }
+        if constexpr (G > 1) {
+            w = __ldcg(reinterpret_cast<const float4*>(ml) + c);
+        } else {
+            const float2 x = __ldcg(ml);
+            w = make_float4(x.x, st.m[1], x.y, 0.f);
+        }
+        const float n0 = fmaxf(st.m[0], w.x), n1 = fmaxf(st.m[1], w.y);
+        const float a0 = exp2f(st.m[0] - n0), a1 = exp2f(st.m[1] - n1);
+        const float b0 = exp2f(w.x - n0), b1 = exp2f(w.y - n1);
+        // first * its weight, then second * its weight on top
+        auto mix = [&](float mine, float a, float theirs, float b) {
+            return before ? fmaf(mine, a, __fmul_rn(theirs, b)) : fmaf(theirs, b, __fmul_rn(mine, a));
+        };
+        st.m[0] = n0;
+        st.m[1] = n1;
+        st.l[0] = mix(st.l[0], a0, w.z, b0);
+        st.l[1] = mix(st.l[1], a1, w.w, b1);
+#pragma unroll
+        for (int mt = 0; mt < M::KS; ++mt) {
+            st.acc[mt][0] = mix(st.acc[mt][0], a0, v[mt].x, b0);
+            st.acc[mt][1] = mix(st.acc[mt][1], a1, v[mt].y, b1);
+            st.acc[mt][2] = mix(st.acc[mt][2], a0, v[mt].z, b0);
+            st.acc[mt][3] = mix(st.acc[mt][3], a1, v[mt].w, b1);
+        }
+    }
+};
+
+// Merges the n stored pieces of one warp's (b, kv head) in the slots of the
+// leaves off, off + stride, ... in that order: into out (bf16 [G][D]) if
+// given, else over the first of them.  Lane l takes the float4s l, l+32, ...
+// of each piece, all of one head pair; maxima and sums run along (no pass
+// over the pieces before their values).
+template <int D, int G>
+__device__ __noinline__ void merge_raw(const DecodeParams& p, int k0, int off, int stride, int n, int HG, int head,
+                                       int lane, __nv_bfloat16* out) {
+    constexpr int GP = RawPiece<G>::GP;
+    constexpr int N4 = D * G / 4;            // float4s of a piece
+    constexpr int T = (N4 + 31) / 32;        // of a lane
+    constexpr int U = T >= 4 ? 16 / T : 8;   // pieces in flight
+    const int c = lane % GP;
+    auto slot = [&](int i) -> int64_t { return (leaf_slot(k0, off + i * stride) * HG + head) * G; };
+    float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
+    float4 a[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) a[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += U) {
+        float4 v[U][T], w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool there = i0 + u < n;
+            const int64_t s = slot(there ? i0 + u : 0);
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+                v[u][t] = N4 % 32 == 0 || lane + 32 * t < N4
+                              ? __ldcg(reinterpret_cast<const float4*>(p.part_o + s * D) + lane + 32 * t)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+            if constexpr (G > 1) {
+                w[u] = __ldcg(reinterpret_cast<const float4*>(p.part_ml + s) + c);
+            } else {
+                const float2 x = __ldcg(p.part_ml + s);
+                w[u] = make_float4(x.x, x.x, x.y, x.y);
+            }
+            if (!there) w[u] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float n0 = fmaxf(M0, w[u].x), n1 = fmaxf(M1, w[u].y);  // finite from the first piece on
+            const float s0 = exp2f(M0 - n0), s1 = exp2f(M1 - n1);
+            const float w0 = exp2f(w[u].x - n0), w1 = exp2f(w[u].y - n1);
+            M0 = n0;
+            M1 = n1;
+            L0 = L0 * s0 + w[u].z * w0;
+            L1 = L1 * s1 + w[u].w * w1;
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                a[t].x = a[t].x * s0 + v[u][t].x * w0;
+                a[t].y = a[t].y * s1 + v[u][t].y * w1;
+                a[t].z = a[t].z * s0 + v[u][t].z * w0;
+                a[t].w = a[t].w * s1 + v[u][t].w * w1;
+            }
+        }
+    }
+    __syncwarp();  // every lane has read the first slot
+    const float r0 = 1.f / L0, r1 = 1.f / L1;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const int i = lane + 32 * t;
+        if (N4 % 32 != 0 && i >= N4) continue;
+        if (!out) {
+            reinterpret_cast<float4*>(p.part_o + slot(0) * D)[i] = a[t];
+        } else if constexpr (G > 1) {
+            const int r = i / GP, d = 16 * (r / 8) + r % 8;
+            __nv_bfloat16* o = out + 2 * c * D + d;
+            o[0] = __float2bfloat16_rn(a[t].x * r0);
+            o[D] = __float2bfloat16_rn(a[t].y * r1);
+            o[8] = __float2bfloat16_rn(a[t].z * r0);
+            o[D + 8] = __float2bfloat16_rn(a[t].w * r1);
+        } else {
+            const int r = 2 * i, d = 16 * (r / 8) + r % 8;  // rows r and r + 1 (r even: one tile)
+            out[d] = __float2bfloat16_rn(a[t].x * r0);
+            out[d + 8] = __float2bfloat16_rn(a[t].y * r0);
+            out[d + 1] = __float2bfloat16_rn(a[t].z * r0);
+            out[d + 9] = __float2bfloat16_rn(a[t].w * r0);
+        }
+    }
+    if (!out && lane < GP) {
+        if constexpr (G > 1) reinterpret_cast<float4*>(p.part_ml + slot(0))[lane] = make_float4(M0, M1, L0, L1);
+        else p.part_ml[slot(0)] = make_float2(M0, L0);
+    }
+}
+
+// One more arrival at a counter, after the calling warp's writes and before
+// its later reads; true in every lane if it completes `count`.
+__device__ __forceinline__ bool arrive_last(int32_t* counter, int count, int lane) {
+    __syncwarp();
+    int old = 0;
+    if (lane == 0)
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+    old = __shfl_sync(0xffffffffu, old, 0);
+    return old == count - 1;
 }
 
 struct WideDesc {  // one segment, from the producer to the consumers
@@ -284,13 +548,17 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int HG = sh.HG, HS = sh.HS, SPL = 1 << sh.SPL_LOG, WPH = 1 << sh.WPH_LOG, R = sh.R;
 
+    // a stage's scales are 16-byte pieces: one bulk copy each for K and V
+    const bool bulk_scales = I8 && HS % 4 == 0 && p.Hkv % 4 == 0 &&
+                             ((reinterpret_cast<uintptr_t>(p.k_scale) | reinterpret_cast<uintptr_t>(p.v_scale)) & 15) == 0;
+
     if (warp == kWideWarps && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_k)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tmap_v)) : "memory");
     }
     if (warp == 0) {
         for (int r = lane; r < R; r += 32) {
-            mbar_init(&full[r], I8 ? 2 : 1);  // the TMA copies' expectation, and the scales' arrival
+            mbar_init(&full[r], I8 && !bulk_scales ? 2 : 1);  // the copies' expectation, and the scales' arrival
             mbar_init(&empty[r], uint32_t(HS));
         }
         if (lane < S) {
@@ -298,7 +566,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
             mbar_init(&segempty[lane], uint32_t(HG * WPH));
         }
         if (lane < HG) {
-            mbar_init(&partfull[lane], uint32_t(WPH - 1));
+            mbar_init(&partfull[lane], uint32_t(WPH > 1 ? WPH - 1 : 1));
             mbar_init(&partempty[lane], 1);
         }
         if (lane == 0) misc->abort = 0;
@@ -363,60 +631,114 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
     if (warp == kWideWarps) {
         // ======================= producer warp =======================
         uint32_t stage_i = 0, seg_i = 0;
+        int slot0 = 0;       // slot of the batch's first stage
+        uint32_t use0 = 0;   // parity of that slot's use
         const int C = R < 32 ? R : 32;
         bool ok = true;
         const uint64_t pol = policy_evict_first();
         const uint32_t stage_tx = uint32_t(2 * HS * kTile);
-        int b = misc->b0;
-        int32_t L = misc->L0;
-        WindowPages pages(L, wp.window, wp.sinks);
-        int64_t unit = pages.np + p.seg_weight;
-        int hg = int((p_start - misc->pre0) / unit);
-        int64_t u0 = misc->pre0 + int64_t(hg) * unit;  // line position of (b, hg)'s first page
-        while (ok && u0 < p_end) {
-            const int j = cut_page(p_start, u0, pages.np, sh.snap);
-            const int npg = cut_page(p_end, u0, pages.np, sh.snap) - j;
-            if (npg > 0) {
-                if (lane == 0) {
-                    const int s = seg_i % S;
-                    if (seg_i >= S) ok = mbar_wait(&segempty[s], ((seg_i / S) - 1) & 1, abort);
-                    if (ok) {
-                        // the CTAs of the segment's first and last page
-                        int k0 = split.owner(u0), k1 = split.owner(u0 + pages.np - 1);
-                        if (cut_page(split.start(k0 + 1), u0, pages.np, sh.snap) == 0) ++k0;
-                        if (cut_page(split.start(k1), u0, pages.np, sh.snap) == pages.np) --k1;
-                        descs[s] = WideDesc{b, hg, j, npg, L, k0, k1, 0};
-                        mbar_arrive(&segfull[s]);
-                    }
+
+        // The segments of the share in order; block ids are read one batch
+        // of stages ahead, over segment ends too, so that no page waits for
+        // the block table.
+        struct Seg {
+            int32_t b, hg, L, j, npg;
+            int64_t u0;  // line position of its first page
+        };
+        auto pages_of = [&](const Seg& g) { return WindowPages(g.L, wp.window, wp.sinks); };
+        auto cut = [&](Seg& g, int32_t np) {
+            g.j = cut_page(p_start, g.u0, np, sh.snap);
+            g.npg = cut_page(p_end, g.u0, np, sh.snap) - g.j;
+        };
+        // The segment after g (u0 >= p_end: none); L_next: the length of
+        // sequence g.b + 1, read ahead.
+        auto after = [&](const Seg& g, int32_t L_next) {
+            Seg n = g;
+            do {
+                n.u0 += pages_of(n).np + p.seg_weight;
+                if (n.u0 >= p_end) return n;
+                if (++n.hg == p.NG) {
+                    n.hg = 0;
+                    ++n.b;
+                    n.L = L_next;
+                    while (n.L == 0) n.L = clamp_len<16>(p, ++n.b, false);
+                    if (n.b + 1 < p.B) L_next = clamp_len<16>(p, n.b + 1, false);
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                // one lane per stage: HS heads' K tiles, then their V tiles
-                const int32_t* bt = p.block_tables + int64_t(b) * p.M;
-                const int tile0 = hg * HG;
-                const int nst = npg << sh.SPL_LOG;
-                for (int c0 = 0; ok && c0 < nst; c0 += C) {
-                    const int n = (nst - c0) < C ? (nst - c0) : C;
-                    bool lane_ok = true;
-                    if (lane < n) {
-                        const int x = c0 + lane;
-                        int32_t blk = __ldg(bt + pages.page(j + (x >> sh.SPL_LOG)));
-                        if (blk < 0 || blk >= p.NB) {
-                            raise_error(PA_DEVERR_BLOCK_ID);
-                            blk = 0;
-                        }
-                        const int sub = x & (SPL - 1);
-                        const uint32_t i = stage_i + x;
-                        const int slot = int(i % R);
-                        const uint32_t use = i / R;
-                        if (use > 0) lane_ok = mbar_wait(&empty[slot], (use - 1) & 1, abort);
-                        if (lane_ok) {
-                            uint8_t* st = ring + slot * 2 * sh.stage_k;
-                            mbar_arrive_expect_tx(&full[slot], stage_tx);
-                            const int tile = blk * p.Hkv + tile0 + sub * HS;
-                            tma_load_4d(st, &p.tmap_k, 0, 0, 0, tile, &full[slot], pol);
-                            tma_load_4d(st + sh.stage_k, &p.tmap_v, 0, 0, 0, tile, &full[slot], pol);
-                            if constexpr (I8) {
-                                float* sc = scales + slot * 16;
+                cut(n, pages_of(n).np);
+            } while (n.npg == 0);
+            return n;
+        };
+        // Block id of this lane's stage c0 + lane of segment g (0 past its end).
+        auto block_of = [&](const Seg& g, int c0) -> int32_t {
+            const int x = c0 + lane;
+            if (lane >= C || x >= g.npg << sh.SPL_LOG) return 0;
+            return __ldg(p.block_tables + int64_t(g.b) * p.M + pages_of(g).page(g.j + (x >> sh.SPL_LOG)));
+        };
+
+        Seg seg;
+        seg.b = misc->b0;
+        seg.L = misc->L0;
+        const int64_t unit0 = pages_of(seg).np + p.seg_weight;
+        seg.hg = int((p_start - misc->pre0) / unit0);
+        seg.u0 = misc->pre0 + int64_t(seg.hg) * unit0;
+        cut(seg, pages_of(seg).np);
+        if (seg.npg == 0) seg = after(seg, seg.b + 1 < p.B ? clamp_len<16>(p, seg.b + 1, false) : 0);
+        int32_t blk = seg.u0 < p_end ? block_of(seg, 0) : 0;
+        while (ok && seg.u0 < p_end) {
+            const int32_t L_next = seg.b + 1 < p.B ? clamp_len<16>(p, seg.b + 1, false) : 0;
+            if (lane == 0) {
+                const int s = seg_i % S;
+                if (seg_i >= S) ok = mbar_wait(&segempty[s], ((seg_i / S) - 1) & 1, abort);
+                if (ok) {
+                    // the CTAs of the segment's first and last page
+                    const int np = pages_of(seg).np;
+                    int k0 = split.owner(seg.u0), k1 = split.owner(seg.u0 + np - 1);
+                    if (cut_page(split.start(k0 + 1), seg.u0, np, sh.snap) == 0) ++k0;
+                    if (cut_page(split.start(k1), seg.u0, np, sh.snap) == np) --k1;
+                    descs[s] = WideDesc{seg.b, seg.hg, seg.j, seg.npg, seg.L, k0, k1, 0};
+                    mbar_arrive(&segfull[s]);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            // one lane per stage: HS heads' K tiles, then their V tiles
+            const int tile0 = seg.hg * HG;
+            const int nst = seg.npg << sh.SPL_LOG;
+            Seg next = seg;
+            for (int c0 = 0; ok && c0 < nst; c0 += C) {
+                int32_t blk_next;
+                if (c0 + C < nst) {
+                    blk_next = block_of(seg, c0 + C);
+                } else {
+                    next = after(seg, L_next);
+                    blk_next = next.u0 < p_end ? block_of(next, 0) : 0;
+                }
+                const int n = (nst - c0) < C ? (nst - c0) : C;
+                bool lane_ok = true;
+                if (lane < n) {
+                    if (blk < 0 || blk >= p.NB) {
+                        raise_error(PA_DEVERR_BLOCK_ID);
+                        blk = 0;
+                    }
+                    const int x = c0 + lane;
+                    int slot = slot0 + lane;  // of stage stage_i + x, in its use of parity `use`
+                    uint32_t use = use0;
+                    if (slot >= R) {
+                        slot -= R;
+                        use ^= 1;
+                    }
+                    if (stage_i + x >= uint32_t(R)) lane_ok = mbar_wait(&empty[slot], use ^ 1, abort);
+                    if (lane_ok) {
+                        uint8_t* st = ring + slot * 2 * sh.stage_k;
+                        mbar_arrive_expect_tx(&full[slot], stage_tx + (bulk_scales ? uint32_t(8 * HS) : 0u));
+                        const int tile = blk * p.Hkv + tile0 + (x & (SPL - 1)) * HS;
+                        tma_load_4d(st, &p.tmap_k, 0, 0, 0, tile, &full[slot], pol);
+                        tma_load_4d(st + sh.stage_k, &p.tmap_v, 0, 0, 0, tile, &full[slot], pol);
+                        if constexpr (I8) {
+                            float* sc = scales + slot * 16;
+                            if (bulk_scales) {
+                                bulk_g2s(sc, p.k_scale + tile, uint32_t(4 * HS), &full[slot]);
+                                bulk_g2s(sc + 8, p.v_scale + tile, uint32_t(4 * HS), &full[slot]);
+                            } else {
                                 for (int h = 0; h < HS; ++h) {
                                     cp_async4(sc + h, p.k_scale + tile + h);
                                     cp_async4(sc + 8 + h, p.v_scale + tile + h);
@@ -425,21 +747,18 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
                             }
                         }
                     }
-                    ok = __all_sync(0xffffffffu, lane_ok);
                 }
-                stage_i += nst;
-                ++seg_i;
+                ok = __all_sync(0xffffffffu, lane_ok);
+                blk = blk_next;
+                slot0 += n;
+                if (slot0 >= R) {
+                    slot0 -= R;
+                    use0 ^= 1;
+                }
             }
-            u0 += unit;
-            if (u0 < p_end && ++hg == p.NG) {
-                hg = 0;
-                do {
-                    ++b;
-                    L = clamp_len<16>(p, b, false);
-                } while (L == 0);
-                pages = WindowPages(L, wp.window, wp.sinks);
-                unit = pages.np + p.seg_weight;
-            }
+            stage_i += nst;
+            ++seg_i;
+            seg = next;
         }
         if (ok && lane == 0) {  // end-of-share marker
             const int s = seg_i % S;
@@ -465,8 +784,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
     const int head = warp % HG, part = warp / HG;
     const int sub = head / HS, pos = head - sub * HS;  // stage of a page, tile of the stage
     uint32_t page_base = 0, seg_i = 0;
+    // this warp's next stage: R is a multiple of the step, so its pages recur
+    // in the same slots and every parity wait is exact
+    const int step = SPL << sh.WPH_LOG;
+    int slot = (part << sh.SPL_LOG) + sub;
+    uint32_t phase = 0;
     const int64_t hgG = int64_t(HG) * G;
     float4* mine = reinterpret_cast<float4*>(smem + lay.parts + ((part - 1) * HG + head) * part_bytes(D));  // part > 0
+    const uint32_t tiles = smem_u32(ring) + uint32_t(pos * kTile);  // this head's K tile in stage 0
     MathT st;
 
     while (true) {
@@ -481,20 +806,56 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
         st.load_q_global(p.q + row * (D * 2), lane, p.qscale);
         st.reset();
         const WindowPages pages(d.L, wp.window, wp.sinks);
-        // this part's pages: those whose running number is `part` modulo WPH,
-        // so (R being a multiple of SPL * WPH) its stages recur in the same
-        // slots and every parity wait is exact
-        for (int k = int((part - page_base) & uint32_t(WPH - 1)); k < d.npg; k += WPH) {
-            const uint32_t i = ((page_base + uint32_t(k)) << sh.SPL_LOG) + sub;
-            const int slot = int(i % R);
+        // this part's pages: those whose running number is `part` modulo WPH
+        auto advance = [&]() {
+            slot += step;
+            if (slot >= R) {
+                slot -= R;
+                phase ^= 1;
+            }
+        };
+        // the tokens of listed page k that count (whole inside the window)
+        auto seen = [&](int k) -> uint32_t {
             const int pg = pages.page(d.j0 + k);
-            const uint32_t vis = visible_tokens(pg, d.L, pages.first, wp.sinks);
-            if (!mbar_wait(&full[slot], (i / R) & 1, abort)) return;
-            uint8_t* kt = ring + slot * 2 * sh.stage_k + pos * kTile;
-            uint8_t* vt = kt + sh.stage_k;
-            if constexpr (I8) {
-                st.page(kt, vt, vis, scales[slot * 16 + pos], scales[slot * 16 + 8 + pos], lane);
-            } else {
+            return pg * 16 >= pages.first && pg * 16 + 16 <= d.L ? 0xffffu
+                                                                 : visible_tokens(pg, d.L, pages.first, wp.sinks);
+        };
+        int k = int((part - page_base) & uint32_t(WPH - 1));
+        if constexpr (I8) {
+            while (k < d.npg) {  // this part's pages in twos
+                uint32_t kt[2], vt[2], vis[2];
+                float ks[2], vs[2];
+                int slots[2];
+                const bool two = k + WPH < d.npg;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i == 1 && !two) {
+                        kt[1] = kt[0], vt[1] = vt[0], ks[1] = ks[0], vs[1] = vs[0], vis[1] = 0u;
+                        break;
+                    }
+                    slots[i] = slot;
+                    vis[i] = seen(k);
+                    if (!mbar_wait(&full[slot], phase, abort)) return;
+                    kt[i] = tiles + uint32_t(slot * 2 * sh.stage_k);
+                    vt[i] = kt[i] + uint32_t(sh.stage_k);
+                    ks[i] = scales[slot * 16 + pos];
+                    vs[i] = scales[slot * 16 + 8 + pos];
+                    k += WPH;
+                    advance();
+                }
+                st.pages(kt, vt, vis, ks, vs, lane);
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&empty[slots[0]]);
+                    if (two) mbar_arrive(&empty[slots[1]]);
+                }
+            }
+        } else {
+            for (; k < d.npg; k += WPH) {
+                const uint32_t vis = seen(k);
+                if (!mbar_wait(&full[slot], phase, abort)) return;
+                uint8_t* kt = ring + slot * 2 * sh.stage_k + pos * kTile;
+                uint8_t* vt = kt + sh.stage_k;
                 if (vis != 0xffffu) {
                     // rows that do not count may hold anything (NaN included): clear them
                     // in the V tile so that 0 * row stays 0 in the tensor core
@@ -508,9 +869,10 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
                     fence_proxy_async_smem();  // before the stage is refilled by TMA
                 }
                 st.template page<true>(kt, vt, int(vis), lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[slot]);
+                advance();
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[slot]);
         }
 
         // ---- the parts meet: part 0 takes the others' states over in order ----
@@ -530,7 +892,14 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
             ++seg_i;
             continue;
         }
-        if (!mbar_wait(&partfull[head], seg_i & 1, abort)) return;
+        // A cut segment's first piece ends its CTA's share, its last piece
+        // starts another's, so with two pieces the last one is usually there
+        // already: its arrival is looked up while the parts meet.
+        const int nk = d.k1 - d.k0 + 1;
+        const int leaf = int(blockIdx.x) - d.k0;
+        int32_t* top = p.counters + int64_t(d.b) * p.Hkv + g;
+        const bool there = nk == 2 && leaf == 0 && ld_acquire_gpu(top) == 1;
+        if (WPH > 1 && !mbar_wait(&partfull[head], seg_i & 1, abort)) return;
         for (int w = 1; w < WPH; ++w) {
             if (!has_pages(w)) continue;
             const float4* o =
@@ -557,72 +926,46 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
         if (lane == 0) mbar_arrive(&partempty[head]);
 
         // ---- segment end: this (b, g)'s result, or its piece and the merge of the pieces ----
-        const int nk = d.k1 - d.k0 + 1;
-        const int leaf = int(blockIdx.x) - d.k0;
-        int32_t* top = p.counters + int64_t(d.b) * p.Hkv + g;
-        if (nk == 1) {
-            st.finish();
-            st.store_out(p.out + row * D, lane);
-        } else if (nk <= kFastMergePieces) {
-            // ticket first; the second piece to finish merges the first one's
-            // published partial with its own registers, in leaf order
-            if (ticket(top, nk, lane)) {
-                const int64_t sl = leaf_slot(d.k0, 1 - leaf);
-                const int* flag = p.slot_sync + sl * HG + head;
-                const uint64_t t0 = globaltimer_ns();
-                for (uint32_t it = 0; ld_acquire_gpu(flag) == 0; ++it) {  // set right after its ticket
-                    __nanosleep(32);
-                    if ((it & 63u) == 63u && globaltimer_ns() - t0 > kWaitLimitNs) {
-                        raise_error(PA_DEVERR_TIMEOUT);
-                        break;
-                    }
-                }
-                __syncwarp();
-                const int64_t ps = sl * hgG + int64_t(head) * G;
-                typename MathT::Piece other;
-                st.piece_load(other, p.part_o + ps * D, p.part_ml + ps, lane);
-                st.finish();
-                st.store_merged2(other, leaf == 0, p.out + row * D, lane);
-                __syncwarp();
-                if (lane == 0) {
-                    p.slot_sync[sl * HG + head] = 0;
-                    *top = 0;
-                }
-            } else {
-                const int64_t ps = leaf_slot(d.k0, leaf) * hgG + int64_t(head) * G;
-                st.finish();
-                st.store_partial(p.part_o + ps * D, p.part_ml + ps, nullptr, nullptr, lane);
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) st_release_gpu(p.slot_sync + leaf_slot(d.k0, leaf) * HG + head, 1);
-            }
-        } else {
-            const int64_t ps = leaf_slot(d.k0, leaf) * hgG + int64_t(head) * G;
-            st.finish();
-            st.store_partial(p.part_o + ps * D, p.part_ml + ps, nullptr, nullptr, lane);
-            __threadfence();
-            __syncwarp();
+        auto slot_of = [&](int lf) -> int64_t { return (leaf_slot(d.k0, lf) * HG + head) * G; };
+        const int64_t ps = slot_of(leaf);
+        if constexpr (I8) st.join_halves();
+        st.finish();
+        bool last = nk == 1 || __all_sync(0xffffffffu, there);
+        if (!last) {
+            RawPiece<G>::store(st, p.part_o + ps * D, p.part_ml + ps, lane);
             if (nk <= kMergeFanIn) {
-                if (ticket(top, nk, lane)) {
-                    merge_pieces<D, G>(p, d.k0, 0, 1, nk, HG, head, lane, p.out + row * D);
+                last = arrive_last(top, nk, lane);
+                if (last && nk > 2) {
+                    merge_raw<D, G>(p, d.k0, 0, 1, nk, HG, head, lane, p.out + row * D);
                     if (lane == 0) *top = 0;
+                    last = false;
                 }
             } else {
-                const int first = leaf - leaf % kMergeFanIn;
-                const int runs = (nk + kMergeFanIn - 1) / kMergeFanIn;
-                const int in_run = nk - first < kMergeFanIn ? nk - first : kMergeFanIn;
+                // runs of about sqrt(nk) pieces, each merged by the last of its
+                // pieces to arrive, then the runs by the last of them
+                int fan = kMergeFanIn;
+                while (fan * fan < nk) ++fan;
+                const int first = leaf - leaf % fan;
+                const int runs = (nk + fan - 1) / fan;
+                const int in_run = nk - first < fan ? nk - first : fan;
                 int32_t* gc = p.slot_sync + leaf_slot(d.k0, first) * HG + head;
-                if (ticket(gc, in_run, lane)) {
-                    merge_pieces<D, G>(p, d.k0, first, 1, in_run, HG, head, lane, nullptr);
+                if (arrive_last(gc, in_run, lane)) {
+                    merge_raw<D, G>(p, d.k0, first, 1, in_run, HG, head, lane, nullptr);
                     if (lane == 0) *gc = 0;
-                    __threadfence();
-                    __syncwarp();
-                    if (ticket(top, runs, lane)) {
-                        merge_pieces<D, G>(p, d.k0, 0, kMergeFanIn, runs, HG, head, lane, p.out + row * D);
+                    if (arrive_last(top, runs, lane)) {
+                        merge_raw<D, G>(p, d.k0, 0, fan, runs, HG, head, lane, p.out + row * D);
                         if (lane == 0) *top = 0;
                     }
                 }
             }
+        }
+        if (last) {
+            if (nk == 2) {
+                const int64_t os = slot_of(1 - leaf);
+                RawPiece<G>::fold(st, p.part_o + os * D, p.part_ml + os, leaf == 1, lane);
+                if (lane == 0) *top = 0;
+            }
+            st.store_out(p.out + row * D, lane);
         }
         ++seg_i;
     }
