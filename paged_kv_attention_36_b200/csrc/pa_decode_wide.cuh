@@ -26,6 +26,8 @@
 //     the kernel before it.
 #pragma once
 
+#include <type_traits>
+
 #include "pa_decode.cuh"
 #include "pa_tcgen05.cuh"
 
@@ -44,14 +46,14 @@ template <bool B_UNSIGNED>
 __device__ __forceinline__ void imma_16832(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
                                            const int (&c0)[4]) {
     if constexpr (B_UNSIGNED)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k32.row.col.s32.s8.u8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%10, %11, %12, %13};"
             : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "r"(c0[0]), "r"(c0[1]), "r"(c0[2]),
               "r"(c0[3]));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%10, %11, %12, %13};"
             : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
@@ -83,19 +85,19 @@ __host__ __device__ __forceinline__ int32_t cut_page(int64_t t, int64_t u0, int3
 //
 //   q = qmax / 32512 * (256 hi + lo), hi and lo signed: off by at most 2^-16
 //     of the row's largest value.  S = 256 (K hi) + K lo, exact in integers.
-//   P: for the 32 tokens of a page pair, y = logit + log2(v_scale) and its
-//     maximum over the pair; w = 2^(y - max) = (256 hi + lo) / 65535, hi and
-//     lo unsigned.  A token's weight is off by at most 2^-17 of the heaviest
-//     contribution of its own pair, whatever the other pairs' weights or the
-//     other blocks' scales are.
+//   P: for the tokens of a step (4 pages, 2 at head_dim 128), y = logit +
+//     log2(v_scale) and its maximum over the step; w = 2^(y - max) =
+//     (256 hi + lo) / 65535, hi and lo unsigned.  A token's weight is off by
+//     at most 2^-17 of the heaviest contribution of its own step, whatever
+//     the other steps' weights or the other blocks' scales are.
 //
-// With up to four heads the halves share an mma: columns 0-3 take the high
-// halves of the heads, columns 4-7 the low ones; both sums of a head meet
-// with one shuffle (S in every page, O once at the end).  With eight heads
-// each half has an mma of its own.  Sums of a pair stay below 2^22 and become
-// fp32 by one subtraction (kIntBase); the state (m, l, O) is fp32.  l comes
+// With up to four heads the halves of P share an mma: columns 0-3 take the
+// high halves, columns 4-7 the low ones of the same heads (S has each head
+// in both), and the two sums meet at the end.  With eight heads each half
+// has an mma of its own.  Sums of a step stay below 2^22 and become fp32 by
+// one subtraction (kIntBase); the state (m, l, O) is fp32.  l comes
 // from the same w, unrounded: 2^(logit - m) = w * 2^(max - m - log2(v_scale)).
-// m follows the pair maxima lazily (raised when one passes it by 15).
+// m follows the maxima of the steps lazily (raised when one passes it by 15).
 template <int D, int G>
 struct I8Math : MmaMath<D, G, 16> {
     using Base = MmaMath<D, G, 16>;
@@ -106,7 +108,8 @@ struct I8Math : MmaMath<D, G, 16> {
     static constexpr int kElemBytes = 1;
     static constexpr bool kShared = G <= 4;  // high and low halves share an mma
     static constexpr int NQ = kShared ? 1 : 2;
-    uint32_t qi[NQ][D / 32][2];  // q's halves as B fragments
+    static constexpr int kPages = D == 64 ? 4 : 2;  // of a softmax step
+    uint32_t qi[2][D / 32][2];   // q's halves as B fragments
     float qs[2];                 // scale * log2(e) * qmax / 32512 of this lane's two heads
     uint32_t koff[D / 32];       // this lane's K row, for each 32 columns
 
@@ -148,12 +151,8 @@ struct I8Math : MmaMath<D, G, 16> {
                     hi |= uint32_t(up & 0xff) << (8 * e);
                     lo |= uint32_t((q16 - (up << 8)) & 0xff) << (8 * e);
                 }
-                if constexpr (kShared) {
-                    qi[0][j][i] = n < 4 ? hi : lo;
-                } else {
-                    qi[0][j][i] = hi;
-                    qi[NQ - 1][j][i] = lo;
-                }
+                qi[0][j][i] = hi;
+                qi[1][j][i] = lo;
             }
         // columns 2c and 2c + 1 of S are this lane's; their rows lie in lanes 4 n ..
         const float unit = qscale * (top / 32512.f);
@@ -164,36 +163,39 @@ struct I8Math : MmaMath<D, G, 16> {
         for (int j = 0; j < D / 32; ++j) koff[j] = uint32_t(k_off(t, 2 * j + (mi >> 1)));
     }
 
-    // Two pages (shared-memory addresses of their K and V tiles), the tokens
+    // NP pages (shared-memory addresses of their K and V tiles), the tokens
     // of `vis` counting (0: the page is not there; its addresses are valid).
-    __device__ __forceinline__ void pages(const uint32_t (&kt)[2], const uint32_t (&vt)[2], const uint32_t (&vis)[2],
-                                          const float (&ks)[2], const float (&vs)[2], int lane) {
+    template <int NP>
+    __device__ __forceinline__ void pages(const uint32_t (&kt)[NP], const uint32_t (&vt)[NP],
+                                          const uint32_t (&vis)[NP], const float (&ks)[NP], const float (&vs)[NP],
+                                          int lane) {
+        static_assert(NP % 2 == 0 && NP * 16 * 255 * 127 < 1 << 22, "whole k32 steps, sums below 2^22");
         constexpr int base[4] = {kIntBase, kIntBase, kIntBase, kIntBase};
-        const bool high = (lane & 3) < 2;  // (kShared) this lane's columns are high halves
-        const float wt = kShared && !high ? 1.f : 256.f;
-        // ---- y = scale * K . q + log2(v_scale) ----
-        float y[2][4], lv[2];
+        // ---- every fragment of K first, then the products of the pages in turn ----
+        int s[NP][2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            int s[NQ][4];
+        for (int j = 0; j < D / 32; ++j) {
+            uint32_t ka[NP][4];
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-                uint32_t a[4];
-                ldsm_x4(a, kt[i] + koff[j]);
+            for (int i = 0; i < NP; ++i) ldsm_x4(ka[i], kt[i] + koff[j]);
 #pragma unroll
-                for (int x = 0; x < NQ; ++x) {
-                    if (j == 0) imma_16832<false>(s[x], a, qi[x][j][0], qi[x][j][1], base);
-                    else imma_16832<false>(s[x], a, qi[x][j][0], qi[x][j][1], s[x]);
+            for (int i = 0; i < NP; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (j == 0) imma_16832<false>(s[i][x], ka[i], qi[x][j][0], qi[x][j][1], base);
+                    else imma_16832<false>(s[i][x], ka[i], qi[x][j][0], qi[x][j][1], s[i][x]);
                 }
-            }
+        }
+        // ---- y = scale * K . q + log2(v_scale) ----
+        float y[NP][4], lv[NP];
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
             lv[i] = fmaxf(__log2f(vs[i]), -100.f);  // a scale of 0: codes of 0, weight still in l
             const float c[2] = {qs[0] * ks[i], qs[1] * ks[i]};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float v = fmaf(__int_as_float(s[0][e]), wt, -kIntBaseF * wt);
-                if constexpr (kShared) v += __shfl_xor_sync(0xffffffffu, v, 2);
-                else v += __int_as_float(s[NQ - 1][e]) - kIntBaseF;
-                y[i][e] = fmaf(v, c[e & 1], lv[i]);
+                const float hi = __int_as_float(s[i][0][e]) - kIntBaseF, lo = __int_as_float(s[i][1][e]) - kIntBaseF;
+                y[i][e] = fmaf(fmaf(hi, 256.f, lo), c[e & 1], lv[i]);
             }
             if (vis[i] != 0xffffu) {
                 const int t0 = lane >> 2;
@@ -201,9 +203,13 @@ struct I8Math : MmaMath<D, G, 16> {
                 if (!((vis[i] >> (t0 + 8)) & 1)) y[i][2] = y[i][3] = -INFINITY;
             }
         }
-        // ---- the pair's maximum of each head column, and the running one ----
-        float b0 = fmaxf(fmaxf(y[0][0], y[0][2]), fmaxf(y[1][0], y[1][2]));
-        float b1 = fmaxf(fmaxf(y[0][1], y[0][3]), fmaxf(y[1][1], y[1][3]));
+        // ---- the step's maximum of each head column, and the running one ----
+        float b0 = fmaxf(y[0][0], y[0][2]), b1 = fmaxf(y[0][1], y[0][3]);
+#pragma unroll
+        for (int i = 1; i < NP; ++i) {
+            b0 = fmax3(b0, y[i][0], y[i][2]);
+            b1 = fmax3(b1, y[i][1], y[i][3]);
+        }
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
             b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, off));
@@ -216,9 +222,9 @@ struct I8Math : MmaMath<D, G, 16> {
             m[1] = n1;
         }
         // ---- weights; l; the 16-bit weights as B fragments ----
-        uint32_t pb[NQ][2];
+        uint32_t pb[NQ][NP];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NP; ++i) {
             const float w0 = ex2_approx(y[i][0] - b0), w1 = ex2_approx(y[i][1] - b1);
             const float w2 = ex2_approx(y[i][2] - b0), w3 = ex2_approx(y[i][3] - b1);
             l[0] = fmaf(w0 + w2, ex2_approx(b0 - m[0] - lv[i]), l[0]);
@@ -236,20 +242,26 @@ struct I8Math : MmaMath<D, G, 16> {
             }
         }
         // ---- O^T += V^T . P^T, two m-tiles (32 rows of V^T) per ldmatrix ----
-        const float f0 = ex2_approx(b0 - m[0]) * (1.f / 65535.f) * wt;
-        const float f1 = ex2_approx(b1 - m[1]) * (1.f / 65535.f) * wt;
+        const float wt = kShared && (lane & 3) >= 2 ? 1.f / 65535.f : 256.f / 65535.f;
+        const float f0 = ex2_approx(b0 - m[0]) * wt, f1 = ex2_approx(b1 - m[1]) * wt;
         const uint64_t f2 = f2_pack(f0, f1), down = f2_pack(-kIntBaseF, -kIntBaseF);
 #pragma unroll
         for (int j = 0; j < KS / 2; ++j) {
-            uint32_t r0[4], r1[4];
-            ldsm_x4(r0, vt[0] + uint32_t((32 * j + lane) * 16));
-            ldsm_x4(r1, vt[1] + uint32_t((32 * j + lane) * 16));
+            uint32_t va[NP][4];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) ldsm_x4(va[i], vt[i] + uint32_t((32 * j + lane) * 16));
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                const uint32_t a[4] = {r0[2 * t], r0[2 * t + 1], r1[2 * t], r1[2 * t + 1]};
                 int o[NQ][4];
 #pragma unroll
-                for (int x = 0; x < NQ; ++x) imma_16832<true>(o[x], a, pb[x][0], pb[x][1], base);
+                for (int i = 0; i < NP; i += 2) {
+                    const uint32_t a[4] = {va[i][2 * t], va[i][2 * t + 1], va[i + 1][2 * t], va[i + 1][2 * t + 1]};
+#pragma unroll
+                    for (int x = 0; x < NQ; ++x) {
+                        if (i == 0) imma_16832<true>(o[x], a, pb[x][i], pb[x][i + 1], base);
+                        else imma_16832<true>(o[x], a, pb[x][i], pb[x][i + 1], o[x]);
+                    }
+                }
                 float* dst = acc[2 * j + t];
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
@@ -822,20 +834,21 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
         };
         int k = int((part - page_base) & uint32_t(WPH - 1));
         if constexpr (I8) {
-            while (k < d.npg) {  // this part's pages in twos
-                uint32_t kt[2], vt[2], vis[2];
-                float ks[2], vs[2];
-                int slots[2];
-                const bool two = k + WPH < d.npg;
+            // this part's next pages, NP at a time; of the last step only `have` are there
+            auto run = [&](auto count, int have) -> bool {
+                constexpr int NP = decltype(count)::value;
+                uint32_t kt[NP], vt[NP], vis[NP];
+                float ks[NP], vs[NP];
+                int slots[NP];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (i == 1 && !two) {
-                        kt[1] = kt[0], vt[1] = vt[0], ks[1] = ks[0], vs[1] = vs[0], vis[1] = 0u;
-                        break;
+                for (int i = 0; i < NP; ++i) {
+                    if (i >= have) {
+                        kt[i] = kt[0], vt[i] = vt[0], ks[i] = ks[0], vs[i] = vs[0], vis[i] = 0u;
+                        continue;
                     }
                     slots[i] = slot;
                     vis[i] = seen(k);
-                    if (!mbar_wait(&full[slot], phase, abort)) return;
+                    if (!mbar_wait(&full[slot], phase, abort)) return false;
                     kt[i] = tiles + uint32_t(slot * 2 * sh.stage_k);
                     vt[i] = kt[i] + uint32_t(sh.stage_k);
                     ks[i] = scales[slot * 16 + pos];
@@ -843,13 +856,20 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
                     k += WPH;
                     advance();
                 }
-                st.pages(kt, vt, vis, ks, vs, lane);
+                st.template pages<NP>(kt, vt, vis, ks, vs, lane);
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&empty[slots[0]]);
-                    if (two) mbar_arrive(&empty[slots[1]]);
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+                        if (i < have) mbar_arrive(&empty[slots[i]]);
                 }
-            }
+                return true;
+            };
+            constexpr int NP = MathT::kPages;
+            while (k + (NP - 1) * WPH < d.npg)
+                if (!run(std::integral_constant<int, NP>{}, NP)) return;
+            while (k < d.npg)
+                if (!run(std::integral_constant<int, 2>{}, k + WPH < d.npg ? 2 : 1)) return;
         } else {
             for (; k < d.npg; k += WPH) {
                 const uint32_t vis = seen(k);
