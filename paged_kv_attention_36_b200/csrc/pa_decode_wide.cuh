@@ -346,6 +346,8 @@ __host__ __device__ inline WideLayout wide_layout(const WideShape& s, int D) {
     return w;
 }
 
+constexpr int kWideFanIn = 8;  // pieces merged at once; more go in two levels
+
 // ---- pieces of a (b, kv head) that share boundaries cut --------------------------
 // A piece's state goes to its partial slot as it lies in the fragments,
 // unnormalised: float4 (16-row tile mt, row d0, head pair c) at
@@ -953,7 +955,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
         bool last = nk == 1 || __all_sync(0xffffffffu, there);
         if (!last) {
             RawPiece<G>::store(st, p.part_o + ps * D, p.part_ml + ps, lane);
-            if (nk <= kMergeFanIn) {
+            if (nk <= kWideFanIn) {
                 last = arrive_last(top, nk, lane);
                 if (last && nk > 2) {
                     merge_raw<D, G>(p, d.k0, 0, 1, nk, HG, head, lane, p.out + row * D);
@@ -963,7 +965,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
             } else {
                 // runs of about sqrt(nk) pieces, each merged by the last of its
                 // pieces to arrive, then the runs by the last of them
-                int fan = kMergeFanIn;
+                int fan = 2;
                 while (fan * fan < nk) ++fan;
                 const int first = leaf - leaf % fan;
                 const int runs = (nk + fan - 1) / fan;

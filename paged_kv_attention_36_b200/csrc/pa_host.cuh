@@ -70,12 +70,12 @@ int32_t seg_weight_pages(int head_dim, int heads, int eb) {
 int heads_per_stage_max(int D, int eb, int stage_k) { return stage_k / (kBlockSize * D * eb); }
 
 // kv heads per head group: the largest divisor of Hkv that is at most 8
-// (one consumer warp per head) and splits into 1, 2, 4 or 8 equal stages.
-int heads_per_group(int Hkv, int D, int eb, int stage_k) {
+// (one consumer warp per head) and splits into 1, 2, 4, ... max_spl equal stages.
+int heads_per_group(int Hkv, int D, int eb, int stage_k, int max_spl) {
     const int hs = heads_per_stage_max(D, eb, stage_k);
     for (int h = pa::kDecodeWarps; h > 1; --h) {
         if (Hkv % h) continue;
-        for (int spl = 1; spl <= pa::kDecodeWarps; spl *= 2)
+        for (int spl = 1; spl <= max_spl; spl *= 2)
             if (h % spl == 0 && h / spl <= hs) return h;
     }
     return 1;
@@ -229,7 +229,8 @@ bool make_fp8_map(CUtensorMap* map, const void* base, int64_t tiles, int D, int 
 pa_status prepare_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                          const int32_t* context_lens, float scale, void* out, const pa_dims* dims, int grid,
                          void* workspace, size_t workspace_bytes, pa::DecodeParams& p, int eb = 2,
-                         MathKind mk = math_kind(), int stage_k = PA_STAGE_K_BYTES) {
+                         MathKind mk = math_kind(), int stage_k = PA_STAGE_K_BYTES,
+                         int max_spl = pa::kDecodeWarps) {
     if (!dims) return PA_ERR_NULL;
     if (!dims_ok(dims)) return PA_ERR_SHAPE;
     const pa_dims& d = *dims;
@@ -251,7 +252,7 @@ pa_status prepare_decode(const void* q, const void* k_cache, const void* v_cache
     p = pa::DecodeParams{};
     const int64_t rows = int64_t(d.num_blocks) * d.num_kv_heads * d.block_size;
     if (rows >= (int64_t(1) << 31)) return PA_ERR_SHAPE;  // TMA coordinates are int32
-    const int HG = heads_per_group(d.num_kv_heads, d.head_dim, eb, stage_k);
+    const int HG = heads_per_group(d.num_kv_heads, d.head_dim, eb, stage_k, max_spl);
     int SPL = 1;
     while (HG / SPL > heads_per_stage_max(d.head_dim, eb, stage_k) || HG % SPL) SPL *= 2;
     const int HS = HG / SPL;

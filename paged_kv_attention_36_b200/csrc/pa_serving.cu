@@ -174,7 +174,8 @@ pa_status decode_wide(const Call& c, void* workspace, size_t workspace_bytes, vo
     pa::WideParams p;
     const int grid = sm_count();
     pa_status st = prepare_decode(c.q, c.k_cache, c.v_cache, c.block_tables, c.context_lens, c.scale, c.out, c.dims,
-                                  grid, workspace, workspace_bytes, p.d, I8 ? 1 : 2, MathKind::kMma, kWideStageK);
+                                  grid, workspace, workspace_bytes, p.d, I8 ? 1 : 2, MathKind::kMma, kWideStageK,
+                                  /*max_spl=*/1);
     if (st != PA_OK || c.dims->num_seqs == 0) return st;
     if (I8 && (st = scales_ok(c)) != PA_OK) return st;
     p.d.k_scale = c.k_scale;
