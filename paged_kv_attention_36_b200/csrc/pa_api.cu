@@ -100,22 +100,6 @@ pa_status dispatch_decode(int D, int G, const pa::DecodeParams& p, int grid, cud
                                          : dispatch_d_g<MathKind::kSimt, DUMP, APPEND>(D, G, p, grid, s, pdl);
 }
 
-// tcgen05 prefill configurations: BN keys per block, KS blocks in the ring,
-// CPS CTAs per SM.
-template <int D, int BN> constexpr int tc_stages() {
-    return BN == 128 ? (D == 64 ? 4 : 3) : (D == 64 ? 5 : 2);
-}
-
-template <int D, int BN>
-struct TcShape {
-    static constexpr int KS = tc_stages<D, BN>(), CPS = BN == 128 ? 1 : 2;
-    // S buffers: as many as TMEM holds next to O for CPS CTAs per SM
-    static constexpr int NS = (3 * BN + D) * CPS <= 512 ? 3 : 2;
-    using Cfg = pa::TcPrefillCfg<D, BN, KS, NS>;
-    static_assert(CPS * (Cfg::kSmemBytes + 1024) <= 233472, "CTAs per SM by shared memory");
-    static_assert(CPS * Cfg::kTmemCols <= 512, "CTAs per SM by TMEM columns");
-};
-
 template <int D, int G, int BN>
 pa_status launch_prefill_tc(const pa::PrefillParams& p, dim3 grid, cudaStream_t stream) {
     using S = TcShape<D, BN>;

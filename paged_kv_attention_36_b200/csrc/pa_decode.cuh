@@ -127,9 +127,6 @@ struct DecodeParams {
     // fp8 caches: value = e4m3 code * scale[kv head] (null for bf16 caches)
     const float* k_scale;               // [Hkv]
     const float* v_scale;               // [Hkv]
-    // sliding window (WINDOW): the query at position L-1 attends to tokens
-    // t >= L - window and t < sinks
-    int32_t window, sinks;
 };
 
 // One segment of a CTA's share, handed from the producer to the consumers.
@@ -159,34 +156,6 @@ struct Misc {
 constexpr int kMaxRing = 32;  // ring stages a decode CTA may have (Misc::patch)
 static_assert(sizeof(Misc) <= 256, "misc area");
 
-
-// Sliding window with sinks: of a context of L tokens the query sees tokens
-// 0 .. min(sinks, L)-1 and L-window .. L-1.  Only the pages that hold one of
-// them are listed, in order: `ns` pages of sinks before the window's first
-// page, then the window's pages; entry i is page i for i < ns and page
-// i + skip after that.  A page is listed once, whichever tokens of it are
-// seen (visible_tokens).
-struct WindowPages {
-    int32_t first;  // first token of the window
-    int32_t ns, skip, np;
-    __host__ __device__ __forceinline__ WindowPages(int32_t L, int32_t window, int32_t sinks) {
-        first = L > window ? L - window : 0;
-        const int32_t wpage = first / 16, spages = ((sinks < first ? sinks : first) + 15) / 16;
-        ns = spages < wpage ? spages : wpage;
-        skip = wpage - ns;
-        np = (L + 15) / 16 - skip;
-    }
-    __host__ __device__ __forceinline__ int32_t page(int32_t i) const { return i < ns ? i : i + skip; }
-};
-
-// Which of the 16 tokens of page pg a query at the end of L tokens sees.
-__host__ __device__ __forceinline__ uint32_t visible_tokens(int32_t pg, int32_t L, int32_t first, int32_t sinks) {
-    const int32_t t0 = pg * 16;
-    auto below = [](int32_t n) -> uint32_t {  // bits 0 .. n-1
-        return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u;
-    };
-    return below(L - t0) & (~below(first - t0) | below(sinks < L ? sinks - t0 : 16));
-}
 
 // A finished partial is read from global memory (written by other CTAs or
 // by the shared-prefix pass: L2, not L1) or from this warp's shared-memory
@@ -1012,15 +981,11 @@ struct SeqPages {
 
 constexpr int kFewGroups = 4;  // group tables read whole, in one round of loads
 
-template <int BS, bool WINDOW = false>
+template <int BS>
 __device__ __forceinline__ SeqPages seq_pages(const DecodeParams& p, int b, bool report) {
     SeqPages s;
     s.L = clamp_len<BS>(p, b, report);
     s.P = 0;
-    if constexpr (WINDOW) {  // no shared prefixes: np = the pages a window or a sink is in
-        s.np = WindowPages(s.L, p.window, p.sinks).np;
-        return s;
-    }
     if (p.num_groups > 0) {
         // group i holds b when off[i] <= b < off[i+1]
         const int32_t* off = p.group_offsets;
@@ -1334,14 +1299,12 @@ __device__ __forceinline__ void write_block_rows(const DecodeParams& p, const in
     }
 }
 
-template <int D, int G, int BS, int R, bool DUMP, bool APPEND, template <int, int, int> class Math,
-          bool WINDOW = false>
+template <int D, int G, int BS, int R, bool DUMP, bool APPEND, template <int, int, int> class Math>
 __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1) decode_kernel(const __grid_constant__ DecodeParams p) {
     using Cfg = DecodeCfg<D, BS, R, Math<D, G, BS>::kElemBytes>;
     constexpr int NW = Cfg::NW;
     constexpr int S = Cfg::kSegSlots;
     constexpr int NT = Cfg::kThreads;
-    static_assert(!WINDOW || (BS == 16 && !DUMP && !APPEND && !Math<D, G, BS>::kPairPages), "window: plain decode");
     static_assert(NW + 1 <= 16, "block reductions hold 16 warps");
     static_assert(R % Cfg::kMaxSpl == 0, "the stages of a page recur in the same slots");
     static_assert(R <= kMaxRing, "one patch flag per stage");
@@ -1464,7 +1427,7 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1) decode_kernel(cons
         const int b = base + threadIdx.x;
         long long v = 0;
         if (b < p.B) {
-            const SeqPages sp = seq_pages<BS, WINDOW>(p, b, blockIdx.x == 0);
+            const SeqPages sp = seq_pages<BS>(p, b, blockIdx.x == 0);
             sp_mine = sp;
             v = (long long)(sp.np > 0 ? sp.np + p.seg_weight : 0) * p.NG;
             if (sp.L == 0 && (b % int(gridDim.x)) == int(blockIdx.x)) {
@@ -1534,7 +1497,7 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1) decode_kernel(cons
             long long v = 0;
             SeqPages sp{0, 0, 0};
             if (b < p.B) {
-                sp = seq_pages<BS, WINDOW>(p, b, false);
+                sp = seq_pages<BS>(p, b, false);
                 v = (long long)(sp.np > 0 ? sp.np + p.seg_weight : 0) * p.NG;
             }
             long long chunk_total;
@@ -1567,7 +1530,6 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1) decode_kernel(cons
             if (lo < hi) {
                 const int j = Pb + int(lo - u0);  // first page of the segment in b's table
                 const int npg = int(hi - lo);
-                const WindowPages wp(Lb, WINDOW ? p.window : 0x7fffffff, WINDOW ? p.sinks : 0);
                 if (lane == 0) {
                     const int s = seg_i % S;
                     if (seg_i >= S) ok = mbar_wait(&segempty[s], ((seg_i / S) - 1) & 1, abort);
@@ -1594,9 +1556,7 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1) decode_kernel(cons
                     bool lane_ok = true;
                     int32_t blk = 0;
                     if (lane < n) {
-                        int pg = (c0 + lane) >> p.SPL_LOG;
-                        if constexpr (WINDOW) pg = wp.page(j + pg) - j;
-                        blk = __ldg(bt + pg);
+                        blk = __ldg(bt + ((c0 + lane) >> p.SPL_LOG));
                         if (blk < 0 || blk >= p.NB) {
                             raise_error(PA_DEVERR_BLOCK_ID);
                             blk = 0;
@@ -1686,7 +1646,7 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1) decode_kernel(cons
                 hg = 0;
                 do {
                     ++b;
-                    sp = seq_pages<BS, WINDOW>(p, b, false);
+                    sp = seq_pages<BS>(p, b, false);
                 } while (sp.np == 0);
                 Lb = sp.L;
                 Pb = sp.P;
@@ -1747,7 +1707,6 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1) decode_kernel(cons
         st.load_q_global(p.q + row * (D * 2), lane, p.k_scale ? p.qscale * __ldg(p.k_scale + g) : p.qscale);
         st.oscale = p.v_scale ? __ldg(p.v_scale + g) : 1.f;
         st.reset();
-        const WindowPages wp(d.L, WINDOW ? p.window : 0x7fffffff, WINDOW ? p.sinks : 0);
         // The piece that starts at b's first own page carries the shared
         // prefix: the partials of its nz prefix key ranges are folded in after
         // the pages.  When they fit, all of them are copied now (cp.async)
@@ -1820,13 +1779,8 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1) decode_kernel(cons
             if (!mbar_wait(&full[slot], (i / R) & 1, abort)) return;
             uint8_t* kt = ring + slot * Cfg::kStage + pos * Cfg::kTile;
             uint8_t* vt = kt + Cfg::kStageK;
-            int nv;  // the page's tokens that count: their number, or (WINDOW) a bit for each
-            if constexpr (WINDOW) {
-                nv = int(visible_tokens(wp.page(d.j0 + k), d.L, wp.first, p.sinks));
-            } else {
-                const int nv_raw = d.L - (d.j0 + k) * BS;
-                nv = nv_raw < BS ? nv_raw : BS;
-            }
+            const int nv_raw = d.L - (d.j0 + k) * BS;
+            const int nv = nv_raw < BS ? nv_raw : BS;
             bool wrote = false;
             if constexpr (kConsumerPatch) {
                 if (k == patch_k && misc->patch[slot]) {
@@ -1834,16 +1788,7 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1) decode_kernel(cons
                     wrote = true;
                 }
             }
-            if constexpr (WINDOW) {
-                // as below, for every row that does not count
-                wrote = MathT::kZeroMaskedV && nv != 0xffff;
-                for (int x = lane; wrote && x < D / 64 * BS * 8; x += 32) {
-                    const int t = (x >> 3) & (BS - 1);
-                    if (!((nv >> t) & 1))
-                        *reinterpret_cast<uint4*>(vt + (x >> 7) * Cfg::kPanel + t * 128 + (x & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                }
-            } else if (MathT::kZeroMaskedV && nv < BS) {
+            if (MathT::kZeroMaskedV && nv < BS) {
                 // rows past the context may hold anything (NaN included): clear
                 // them in this head's V tile so that 0 * row stays 0 in the tensor core
                 constexpr int NPANEL = D / 64;
@@ -1859,8 +1804,7 @@ __global__ void __launch_bounds__((kDecodeWarps + 1) * 32, 1) decode_kernel(cons
                 __syncwarp();
                 fence_proxy_async_smem();
             }
-            if constexpr (WINDOW) st.template page<true>(kt, vt, nv, lane);
-            else st.page(kt, vt, nv, lane);
+            st.page(kt, vt, nv, lane);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[slot]);
         }

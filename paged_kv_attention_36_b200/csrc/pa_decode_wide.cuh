@@ -65,6 +65,34 @@ __device__ __forceinline__ void imma_16832(int (&c)[4], const uint32_t (&a)[4], 
 constexpr int kIntBase = 0x4B400000;
 constexpr float kIntBaseF = 12582912.f;
 
+// Sliding window with sinks: of a context of L tokens the query sees tokens
+// 0 .. min(sinks, L)-1 and L-window .. L-1.  Only the pages that hold one of
+// them are listed, in order: `ns` pages of sinks before the window's first
+// page, then the window's pages; entry i is page i for i < ns and page
+// i + skip after that.  A page is listed once, whichever tokens of it are
+// seen (visible_tokens).
+struct WindowPages {
+    int32_t first;  // first token of the window
+    int32_t ns, skip, np;
+    __host__ __device__ __forceinline__ WindowPages(int32_t L, int32_t window, int32_t sinks) {
+        first = L > window ? L - window : 0;
+        const int32_t wpage = first / 16, spages = ((sinks < first ? sinks : first) + 15) / 16;
+        ns = spages < wpage ? spages : wpage;
+        skip = wpage - ns;
+        np = (L + 15) / 16 - skip;
+    }
+    __host__ __device__ __forceinline__ int32_t page(int32_t i) const { return i < ns ? i : i + skip; }
+};
+
+// Which of the 16 tokens of page pg a query at the end of L tokens sees.
+__host__ __device__ __forceinline__ uint32_t visible_tokens(int32_t pg, int32_t L, int32_t first, int32_t sinks) {
+    const int32_t t0 = pg * 16;
+    auto below = [](int32_t n) -> uint32_t {  // bits 0 .. n-1
+        return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u;
+    };
+    return below(L - t0) & (~below(first - t0) | below(sinks < L ? sinks - t0 : 16));
+}
+
 // Page at which a share boundary at line position t cuts a segment of np
 // pages that starts at u0: 0 or np where fewer than `snap` pages (or half
 // the segment) would lie before or behind it.

@@ -10,6 +10,7 @@
 #include <mutex>
 
 #include "pa_decode.cuh"
+#include "pa_prefill_tc.cuh"
 
 namespace pa {
 // read_error_word() of pa_serving.cu's kernels (defined there).
@@ -224,6 +225,22 @@ bool make_fp8_map(CUtensorMap* map, const void* base, int64_t tiles, int D, int 
               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
               PA_L2_PROMOTION, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+// tcgen05 prefill configurations: BN keys per block, KS blocks in the ring,
+// CPS CTAs per SM.
+template <int D, int BN> constexpr int tc_stages() {
+    return BN == 128 ? (D == 64 ? 4 : 3) : (D == 64 ? 5 : 2);
+}
+
+template <int D, int BN>
+struct TcShape {
+    static constexpr int KS = tc_stages<D, BN>(), CPS = BN == 128 ? 1 : 2;
+    // S buffers: as many as TMEM holds next to O for CPS CTAs per SM
+    static constexpr int NS = (3 * BN + D) * CPS <= 512 ? 3 : 2;
+    using Cfg = pa::TcPrefillCfg<D, BN, KS, NS>;
+    static_assert(CPS * (Cfg::kSmemBytes + 1024) <= 233472, "CTAs per SM by shared memory");
+    static_assert(CPS * Cfg::kTmemCols <= 512, "CTAs per SM by TMEM columns");
+};
 
 // Shared validation of the decode calls; fills p.
 pa_status prepare_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,

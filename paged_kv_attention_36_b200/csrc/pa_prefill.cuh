@@ -34,6 +34,7 @@ struct PrefillParams {
     int32_t B, Hq, Hkv, NB, M;
     int32_t tiles_per_seq;          // ceil(max_q_len * G / (16 * NW))
     float qscale;                   // scale * log2(e)
+    int32_t window, sinks;          // WINDOW: tokens t > position - window or t < sinks count
 };
 
 template <int D, int G, int NW, int RS>

@@ -83,7 +83,11 @@ struct TcPrefillCfg {
 // against its own pages, causal (PrefillParams, bf16 output).  PREFIX = true:
 // rows (member, query head) of a shared-prefix group against one key split
 // of the group's shared pages, all visible (PrefixParams, fp32 partials).
-template <bool PREFIX, int D, int G, int BN, int KS, int NS, class Params>
+// WINDOW (not PREFIX): only the pages that hold a token some row of the tile
+// sees are streamed, as one list: `ns` pages of sinks, then the pages from the
+// first row's window on, `skip` pages between them left out.  A row sees list
+// keys [0, min(sinks, hi)) and [lo, hi).
+template <bool PREFIX, int D, int G, int BN, int KS, int NS, bool WINDOW = false, class Params>
 __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     using Cfg = TcPrefillCfg<D, BN, KS, NS>;
     static_assert(Cfg::kBM % G == 0, "a tile holds whole tokens (members)");
@@ -110,6 +114,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     int nrows, row0, nkeys;  // rows of the task, the tile's first row, keys staged (0 .. nkeys-1)
     const int32_t* bt;       // block-table entries of the staged pages
     int L = 0, q0 = 0, first_pos = 0, first = 0, P = 0, pg0 = 0;
+    int ns = 0, skip = 0, f0 = 0;  // WINDOW: f0 = list key of the first row's first window token
     if constexpr (!PREFIX) {
         const int b = int(blockIdx.x) / p.tiles_per_seq;
         const int tile = int(blockIdx.x) - b * p.tiles_per_seq;
@@ -133,6 +138,15 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         first_pos = L - q_len;      // position of query token 0
         const int last_row = (row0 + Cfg::kBM < nrows ? row0 + Cfg::kBM : nrows) - 1;
         nkeys = first_pos + last_row / G + 1;  // tokens 0 .. nkeys-1 are visible to some row
+        if constexpr (WINDOW) {
+            const int p0 = first_pos + row0 / G + 1;
+            f0 = p0 > p.window ? p0 - p.window : 0;
+            const int wpage = f0 / 16, spages = ((p.sinks < f0 ? p.sinks : f0) + 15) / 16;
+            ns = spages < wpage ? spages : wpage;
+            skip = wpage - ns;
+            f0 -= skip * 16;
+            nkeys -= skip * 16;
+        }
         bt = p.block_tables + int64_t(b) * p.M;
     } else {
         const int gi = int(blockIdx.x) / p.tiles_per_group;
@@ -164,7 +178,8 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
 
     // Loads in flight while the barriers and TMEM are set up: the page ids of
     // block 0 (producer lanes) and this thread's Q row (softmax warps).
-    const int32_t blk_first = (warp == 0 && lane < Cfg::kPages && lane < pages) ? __ldg(bt + lane) : 0;
+    auto listed = [&](int pg) { return WINDOW && pg >= ns ? pg + skip : pg; };  // table entry of staged page pg
+    const int32_t blk_first = (warp == 0 && lane < Cfg::kPages && lane < pages) ? __ldg(bt + listed(lane)) : 0;
     uint4 qv[D / 8];
     if (warp >= 2) {
         const int r = row0 + (warp & 3) * 32 + lane;
@@ -240,7 +255,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         // overlaps the waits)
         auto page_of = [&](int t) -> int32_t {
             const int pg = t * Cfg::kPages + lane;
-            return (t < nblk && lane < Cfg::kPages && pg < pages) ? __ldg(bt + pg) : 0;
+            return (t < nblk && lane < Cfg::kPages && pg < pages) ? __ldg(bt + listed(pg)) : 0;
         };
         // K runs one block ahead of V: V_j is read one softmax step after K_j
         int nk = 0, nv = 0;  // blocks whose K (V) copies were issued
@@ -328,7 +343,14 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         const int r = row0 + row;
         const bool valid = r < nrows;
         // keys 0 .. lim-1 are visible to this row; its query row
-        const int lim = PREFIX ? nkeys : (valid ? first_pos + r / G + 1 : 1);
+        // (WINDOW: keys [0, sink) and [lo, lim) of the list; rows past the task as its last one)
+        const int pos1 = first_pos + r / G + 1;  // the row's position + 1
+        const int lim = PREFIX ? nkeys : WINDOW ? (valid ? pos1 - skip * 16 : nkeys) : (valid ? pos1 : 1);
+        int lo = 0, sink = 0;
+        if constexpr (WINDOW) {
+            lo = lim + skip * 16 > p.window ? lim - p.window : 0;
+            sink = p.sinks < lim ? p.sinks : lim;
+        }
         const int64_t qrow = int64_t(PREFIX ? first : q0) + r / G;
 
         // Q row into shared memory (128-byte swizzle: 16-byte chunk c of row t at c ^ (t % 8))
@@ -344,7 +366,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         // the sequence's last page, when it is staged and ends inside the context
         const int rem = L & 15;
         const int last_pg = (L - 1) >> 4;
-        const int zero_blk = (!PREFIX && rem != 0 && last_pg < pages) ? last_pg / Cfg::kPages : -1;
+        const int zero_blk = (!PREFIX && !WINDOW && rem != 0 && last_pg < pages) ? last_pg / Cfg::kPages : -1;
 
         const float c = p.qscale;
         float m = -INFINITY, l = 0.f;
@@ -368,7 +390,13 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
                 for (int i = 0; i < BN; ++i) s[i] *= c;
                 ce = 1.f;
             }
-            if (n0 + BN > lim) {
+            if constexpr (WINDOW) {
+                if (!(n0 >= lo && n0 + BN <= lim) && n0 + BN > sink) {
+#pragma unroll
+                    for (int i = 0; i < BN; ++i)
+                        if (n0 + i >= sink && (n0 + i < lo || n0 + i >= lim)) s[i] = -INFINITY;
+                }
+            } else if (n0 + BN > lim) {
 #pragma unroll
                 for (int i = 0; i < BN; ++i)
                     if (n0 + i >= lim) s[i] = -INFINITY;
@@ -384,7 +412,8 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
                 fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])) * ce;
             const float m_new = fmaxf(m, m_blk);
             if (__any_sync(0xffffffffu, m_new > m + 8.f)) {
-                const float alpha = ex2_approx(m - m_new);  // 0 while m = -inf
+                // 0 while m = -inf (WINDOW: the row may not have seen a key yet, O and l are 0)
+                const float alpha = WINDOW && m_new == -INFINITY ? 1.f : ex2_approx(m - m_new);
                 if (j > 0) {
                     ok = __all_sync(0xffffffffu,
                                     mbar_wait_sleep(&v_empty[(j - 1) % KS], uint32_t((j - 1) / KS) & 1, abort));
@@ -405,7 +434,8 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
             }
             // P = 2^(s*ce - m) as bf16 pairs over the first BN/2 columns of the
             // buffer; the exponent and the row sum in packed f32x2 arithmetic
-            const uint64_t ce2 = f2_pack(ce, ce), nm2 = f2_pack(-m, -m);
+            const float mu = WINDOW && m == -INFINITY ? 0.f : m;
+            const uint64_t ce2 = f2_pack(ce, ce), nm2 = f2_pack(-mu, -mu);
             uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
             for (int k = 0; k < BN / 64; ++k) {
@@ -427,7 +457,24 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
                 l += (a0 + a1) + (b0 + b1);
             }
             tmem_st_wait();
-            if (j == zero_blk) {
+            if constexpr (WINDOW) {
+                // V rows of the list that no row of the tile sees: between the
+                // sinks and the first window, and past the context
+                const int gap = p.sinks > n0 ? p.sinks : n0, gap_end = f0 < n0 + BN ? f0 : n0 + BN;
+                const int past = L - skip * 16 > n0 ? L - skip * 16 : n0;
+                const int past_end = pages * 16 < n0 + BN ? pages * 16 : n0 + BN;
+                if (gap < gap_end || past < past_end) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_sleep(&v_full[j % KS], uint32_t(j / KS) & 1, abort));
+                    if (!ok) break;
+                    uint8_t* vz = stages + (j % KS) * Cfg::kStage + Cfg::kKBytes;
+                    for (int i = gt; i < BN * 8 * Cfg::kPanels; i += 128) {
+                        const int pc = i / (BN * 8), rr = i - pc * (BN * 8), n = n0 + (rr >> 3);
+                        if ((n >= gap && n < gap_end) || (n >= past && n < past_end))
+                            *reinterpret_cast<uint4*>(vz + pc * Cfg::kPanelKV + rr * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                }
+            } else if (j == zero_blk) {
                 // V rows rem .. 15 of the last page hold no token of the context
                 ok = __all_sync(0xffffffffu, mbar_wait_sleep(&v_full[j % KS], uint32_t(j / KS) & 1, abort));
                 if (!ok) break;
@@ -531,9 +578,9 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     }
 }
 
-template <int D, int G, int BN, int KS, int CPS, int NS>
+template <int D, int G, int BN, int KS, int CPS, int NS, bool WINDOW = false>
 __global__ void __launch_bounds__(6 * 32, CPS) prefill_tc_kernel(const __grid_constant__ PrefillParams p) {
-    tc_attention_tile<false, D, G, BN, KS, NS>(p);
+    tc_attention_tile<false, D, G, BN, KS, NS, WINDOW>(p);
 }
 
 // The shared-prefix (cascade) pass on tcgen05: grid (group x row tile, kv

@@ -59,6 +59,24 @@ pa_status check_prefill(const Call& c, bool* done) {
     return PA_OK;
 }
 
+void fill_prefill(const Call& c, pa::PrefillParams& p) {
+    const pa_dims& d = *c.dims;
+    p.q = static_cast<const uint8_t*>(c.q);
+    p.cu_q_lens = c.cu_q_lens;
+    p.block_tables = c.block_tables;
+    p.context_lens = c.context_lens;
+    p.out = static_cast<__nv_bfloat16*>(c.out);
+    p.B = d.num_seqs;
+    p.Hq = d.num_q_heads;
+    p.Hkv = d.num_kv_heads;
+    p.NB = d.num_blocks;
+    p.M = d.max_blocks_per_seq;
+    p.tiles_per_seq = int32_t((int64_t(c.max_q_len) * (d.num_q_heads / d.num_kv_heads) + 127) / 128);
+    p.qscale = c.scale * kLog2e;
+    p.window = c.window;
+    p.sinks = c.sinks;
+}
+
 template <bool I8>
 pa_status attend_simple(const Call& c, cudaStream_t s) {
     const pa_dims& d = *c.dims;
@@ -185,18 +203,17 @@ pa_status decode_wide(const Call& c, void* workspace, size_t workspace_bytes, vo
     return by_shape(*c.dims, DecodeWide<I8>{p, grid, static_cast<cudaStream_t>(stream)});
 }
 
-struct DecodeWindow {
-    const pa::DecodeParams& p;
-    int grid;
+struct PrefillWindow {
+    const pa::PrefillParams& p;
+    dim3 grid;
     cudaStream_t stream;
     template <int D, int G>
     pa_status operator()() const {
-        constexpr int R = ring_fit<D>();
-        using Cfg = pa::DecodeCfg<D, kBlockSize, R>;
-        auto kern = pa::decode_kernel<D, G, kBlockSize, R, false, false, pa::MmaMath, true>;
+        using S = TcShape<D, 64>;
+        auto kern = pa::prefill_tc_kernel<D, G, 64, S::KS, S::CPS, S::NS, true>;
         static unsigned attr_done[kMaxDevices];
-        if (!set_smem_once(kern, Cfg::kBaseBytes, attr_done)) return PA_ERR_CUDA;
-        kern<<<grid, Cfg::kThreads, Cfg::kBaseBytes, stream>>>(p);
+        if (!set_smem_once(kern, S::Cfg::kSmemBytes, attr_done)) return PA_ERR_CUDA;
+        kern<<<grid, S::Cfg::kThreads, S::Cfg::kSmemBytes, stream>>>(p);
         return launched();
     }
 };
@@ -309,16 +326,9 @@ extern "C" {
 pa_status pa_decode_window(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                            const int32_t* context_lens, float scale, int32_t window, int32_t sinks, void* out,
                            const pa_dims* dims, void* workspace, size_t workspace_bytes, void* stream) {
-    if (!dims) return PA_ERR_NULL;
-    if (!window_ok(window, sinks)) return PA_ERR_SHAPE;
-    pa::DecodeParams p;
-    const int grid = sm_count();
-    const pa_status st = prepare_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out, dims, grid,
-                                        workspace, workspace_bytes, p, /*eb=*/2, MathKind::kMma);
-    if (st != PA_OK || dims->num_seqs == 0) return st;
-    p.window = window;
-    p.sinks = sinks;
-    return by_shape(*dims, DecodeWindow{p, grid, static_cast<cudaStream_t>(stream)});
+    const Call c{q, nullptr, 1, k_cache, v_cache, nullptr, nullptr, block_tables, context_lens, scale, window, sinks,
+                 out, dims};
+    return decode_wide<false>(c, workspace, workspace_bytes, stream);
 }
 
 pa_status pa_decode_i8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -338,7 +348,15 @@ pa_status pa_prefill_window(const void* q, const int32_t* cu_q_lens, int32_t max
     bool done;
     const pa_status st = check_prefill(c, &done);
     if (st != PA_OK || done) return st;
-    return attend_simple<false>(c, static_cast<cudaStream_t>(stream));
+    const pa_dims& d = *dims;
+    pa::PrefillParams p;
+    const int64_t cache_tiles = int64_t(d.num_blocks) * d.num_kv_heads;
+    if (!make_panel_map(&p.tmap_k, k_cache, cache_tiles, d.head_dim, d.block_size) ||
+        !make_panel_map(&p.tmap_v, v_cache, cache_tiles, d.head_dim, d.block_size))
+        return PA_ERR_CUDA;
+    fill_prefill(c, p);
+    const dim3 grid(unsigned(d.num_seqs * p.tiles_per_seq), unsigned(d.num_kv_heads));
+    return by_shape(d, PrefillWindow{p, grid, static_cast<cudaStream_t>(stream)});
 }
 
 pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_len, const void* k_cache,
