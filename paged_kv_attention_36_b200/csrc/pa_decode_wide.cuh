@@ -831,7 +831,6 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
     const int step = SPL << sh.WPH_LOG;
     int slot = (part << sh.SPL_LOG) + sub;
     uint32_t phase = 0;
-    const int64_t hgG = int64_t(HG) * G;
     float4* mine = reinterpret_cast<float4*>(smem + lay.parts + ((part - 1) * HG + head) * part_bytes(D));  // part > 0
     const uint32_t tiles = smem_u32(ring) + uint32_t(pos * kTile);  // this head's K tile in stage 0
     MathT st;

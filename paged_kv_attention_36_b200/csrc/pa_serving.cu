@@ -3,9 +3,9 @@
 // the position rotation: host-side checks and launches.
 #include <type_traits>
 
-#include "pa_attend_simple.cuh"
 #include "pa_decode_wide.cuh"
 #include "pa_host.cuh"
+#include "pa_prefill_i8.cuh"
 #include "pa_rope.cuh"
 
 bool pa::serving_error_word(unsigned int* bits, bool clear) { return read_error_word(bits, clear); }
@@ -75,34 +75,6 @@ void fill_prefill(const Call& c, pa::PrefillParams& p) {
     p.qscale = c.scale * kLog2e;
     p.window = c.window;
     p.sinks = c.sinks;
-}
-
-template <bool I8>
-pa_status attend_simple(const Call& c, cudaStream_t s) {
-    const pa_dims& d = *c.dims;
-    pa::AttendParams p;
-    p.q = static_cast<const __nv_bfloat16*>(c.q);
-    p.k_cache = c.k_cache;
-    p.v_cache = c.v_cache;
-    p.k_scale = c.k_scale;
-    p.v_scale = c.v_scale;
-    p.cu_q_lens = c.cu_q_lens;
-    p.block_tables = c.block_tables;
-    p.context_lens = c.context_lens;
-    p.out = static_cast<__nv_bfloat16*>(c.out);
-    p.B = d.num_seqs;
-    p.Hq = d.num_q_heads;
-    p.Hkv = d.num_kv_heads;
-    p.NB = d.num_blocks;
-    p.M = d.max_blocks_per_seq;
-    p.window = c.window;
-    p.sinks = c.sinks;
-    p.qscale = c.scale * kLog2e;
-    const int rows = c.cu_q_lens ? c.max_q_len : 1;
-    const dim3 grid(unsigned(d.num_seqs), unsigned((d.num_q_heads + 3) / 4), unsigned(rows < 1024 ? rows : 1024));
-    if (d.head_dim == 64) pa::attend_simple_kernel<64, I8><<<grid, 128, 0, s>>>(p);
-    else pa::attend_simple_kernel<128, I8><<<grid, 128, 0, s>>>(p);
-    return launched();
 }
 
 // fn<D, G>() for the head_dim and GQA group of a call that supported() let through.
@@ -214,6 +186,26 @@ struct PrefillWindow {
         static unsigned attr_done[kMaxDevices];
         if (!set_smem_once(kern, S::Cfg::kSmemBytes, attr_done)) return PA_ERR_CUDA;
         kern<<<grid, S::Cfg::kThreads, S::Cfg::kSmemBytes, stream>>>(p);
+        return launched();
+    }
+};
+
+struct PrefillI8 {
+    const pa::PrefillI8Params& p;
+    dim3 grid;
+    cudaStream_t stream;
+    template <int D, int G>
+    pa_status operator()() const {
+        using Cfg = pa::I8PrefillCfg<D>;
+        auto kern = pa::prefill_i8_kernel<D, G>;
+        // the kernel's setmaxnreg split needs exactly the registers it counts on
+        static const bool regs_ok = [&] {
+            cudaFuncAttributes a;
+            return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == Cfg::kRegs;
+        }();
+        static unsigned attr_done[kMaxDevices];
+        if (!regs_ok || !set_smem_once(kern, Cfg::kSmemBytes, attr_done)) return PA_ERR_CUDA;
+        kern<<<grid, Cfg::kThreads, Cfg::kSmemBytes, stream>>>(p);
         return launched();
     }
 };
@@ -369,7 +361,14 @@ pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_l
     pa_status st = check_prefill(c, &done);
     if (st != PA_OK || done) return st;
     if ((st = scales_ok(c)) != PA_OK) return st;
-    return attend_simple<true>(c, static_cast<cudaStream_t>(stream));
+    pa::PrefillI8Params p{};
+    fill_prefill(c, p.a);
+    p.k_cache = static_cast<const int8_t*>(k_cache);
+    p.v_cache = static_cast<const int8_t*>(v_cache);
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    const dim3 grid(unsigned(dims->num_seqs * p.a.tiles_per_seq), unsigned(dims->num_kv_heads));
+    return by_shape(*dims, PrefillI8{p, grid, static_cast<cudaStream_t>(stream)});
 }
 
 pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
