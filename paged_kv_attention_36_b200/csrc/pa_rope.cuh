@@ -93,18 +93,43 @@ __device__ __forceinline__ void turn_chunks(uint4& lo, uint4& hi, const float (&
         for (int j = 0; j < 4; ++j) w[h][j] = float2_to_bf16x2(x[8 * h + 2 * j], x[8 * h + 2 * j + 1]);
 }
 
-// Rows [h0, h0 + n) of token t, chunk pair c: heads 0 .. Hq-1 are the
-// queries, then the keys, then the values (bf16 caches).
-__device__ __forceinline__ void rope_rows(const RopeParams& p, int64_t t, int h0, int n, int c) {
+// HP rows of token t from head h0 on (heads 0 .. Hq-1 are the queries, then
+// the keys, then the values), chunk pair c.  The angles are read once for
+// the HP rows, and the rows' loads are in flight together.
+template <int HP>
+__device__ __forceinline__ void rope_rows(const RopeParams& p, int t, int h0, int heads, int c) {
     const int32_t slot = __ldg(p.slot_mapping + t);
+    const ChunkPair cp = chunk_pair(c, p.rd, p.interleaved);
     if (slot < 0) return;  // padding
-    const int64_t block = slot / p.bs, offset = slot - block * p.bs;
+    const int32_t block = slot / p.bs, offset = slot - block * p.bs;
     const bool stored = block < p.NB;
     if (!stored && c == 0 && h0 == 0) raise_error(PA_DEVERR_SLOT);
-    const ChunkPair cp = chunk_pair(c, p.rd, p.interleaved);
-    float cs[8], sn[8];
-    if (cp.angle >= 0) {
+    uint4 lo[HP], hi[HP];
+    __nv_bfloat16* dst[HP];
+#pragma unroll
+    for (int i = 0; i < HP; ++i) {
+        const int h = h0 + i;
+        const __nv_bfloat16* src;
+        if (h < p.Hq) {
+            src = p.q + t * p.q_stride + h * p.D;
+            dst[i] = p.q_out + (int64_t(t) * p.Hq + h) * p.D;
+        } else {
+            const bool v = h >= p.Hq + p.Hkv;
+            const int g = h - p.Hq - (v ? p.Hkv : 0);
+            src = v ? p.v_new + t * p.v_stride + g * p.D : p.k_new + t * p.k_stride + g * p.D;
+            dst[i] = static_cast<__nv_bfloat16*>(v ? p.v_cache : p.k_cache) +
+                     ((int64_t(block) * p.Hkv + g) * p.bs + offset) * p.D;
+            if (!stored) dst[i] = nullptr;
+        }
+        if (h >= heads) dst[i] = nullptr;
+        if (dst[i]) {
+            lo[i] = *reinterpret_cast<const uint4*>(src + cp.lo);
+            hi[i] = *reinterpret_cast<const uint4*>(src + cp.hi);
+        }
+    }
+    if (cp.angle >= 0 && h0 < p.Hq + p.Hkv) {
         const float* a = angles(p, t, c == 0 && h0 == 0) + cp.angle;
+        float cs[8], sn[8];
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
             const float4 x = __ldg(reinterpret_cast<const float4*>(a + i));
@@ -112,39 +137,28 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, int64_t t, int h0
             cs[i] = x.x, cs[i + 1] = x.y, cs[i + 2] = x.z, cs[i + 3] = x.w;
             sn[i] = y.x, sn[i + 1] = y.y, sn[i + 2] = y.z, sn[i + 3] = y.w;
         }
+#pragma unroll
+        for (int i = 0; i < HP; ++i)
+            if (dst[i] && h0 + i < p.Hq + p.Hkv) turn_chunks(lo[i], hi[i], cs, sn, p.interleaved);
     }
-    for (int h = h0; h < h0 + n; ++h) {
-        const __nv_bfloat16* src;
-        __nv_bfloat16* dst;
-        bool rotate = cp.angle >= 0;
-        if (h < p.Hq) {
-            src = p.q + t * p.q_stride + int64_t(h) * p.D;
-            dst = p.q_out + (t * p.Hq + h) * p.D;
-        } else {
-            if (!stored) continue;
-            const bool v = h >= p.Hq + p.Hkv;
-            const int g = h - p.Hq - (v ? p.Hkv : 0);
-            src = v ? p.v_new + t * p.v_stride + int64_t(g) * p.D : p.k_new + t * p.k_stride + int64_t(g) * p.D;
-            dst = static_cast<__nv_bfloat16*>(v ? p.v_cache : p.k_cache) +
-                  ((block * p.Hkv + g) * p.bs + offset) * p.D;
-            rotate = rotate && !v;
+#pragma unroll
+    for (int i = 0; i < HP; ++i)
+        if (dst[i]) {
+            *reinterpret_cast<uint4*>(dst[i] + cp.lo) = lo[i];
+            *reinterpret_cast<uint4*>(dst[i] + cp.hi) = hi[i];
         }
-        uint4 lo = *reinterpret_cast<const uint4*>(src + cp.lo), hi = *reinterpret_cast<const uint4*>(src + cp.hi);
-        if (rotate) turn_chunks(lo, hi, cs, sn, p.interleaved);
-        *reinterpret_cast<uint4*>(dst + cp.lo) = lo;
-        *reinterpret_cast<uint4*>(dst + cp.hi) = hi;
-    }
 }
 
 // One thread per chunk pair of HP consecutive rows of a token.
 template <int HP>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
-    const int heads = p.Hq + 2 * p.Hkv, groups = (heads + HP - 1) / HP, cpr = p.D / 16;
-    const int64_t i = int64_t(blockIdx.x) * kRopeThreads + threadIdx.x;
-    const int64_t t = i / (groups * cpr);
-    if (t >= p.T) return;
-    const int r = int(i - t * (groups * cpr)), h0 = r / cpr * HP;
-    rope_rows(p, t, h0, heads - h0 < HP ? heads - h0 : HP, r % cpr);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t heads = p.Hq + 2 * p.Hkv, cpr = p.D / 16, per_token = (heads + HP - 1) / HP * cpr;
+    const uint32_t i = blockIdx.x * uint32_t(kRopeThreads) + threadIdx.x;
+    const uint32_t t = i / per_token, r = i - t * per_token;
+    if (t >= uint32_t(p.T)) return;
+    rope_rows<HP>(p, int(t), int(r / cpr) * HP, int(heads), int(r % cpr));
 }
 
 // ---- 8-bit caches ------------------------------------------------------------
@@ -168,11 +182,42 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 // Largest magnitude as bits: non-finite values compare above finite ones, NaN highest.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-__device__ __forceinline__ int quantize(float x, float scale) {
-    if (!(scale > 0.f)) return 0;
-    const int c = __float2int_rn(__fdiv_rn(x, scale));
-    return c > 127 ? 127 : c < -127 ? -127 : c;
-}
+// round(x / scale) of four values as bytes, the division and the rounding IEEE
+// fp32 (ties to even).  x * (1/scale) is off by at most 2 ulp of the quotient,
+// so unless it comes within 2^-13 of a tie it rounds to the same code; those
+// few, and scales whose reciprocal leaves the normal range, are divided.
+struct Quantizer {
+    float scale, inv;
+    bool divide;
+    __device__ __forceinline__ explicit Quantizer(float s) : scale(s) {
+        divide = !(s > 1e-35f && s < 1e35f);
+        inv = divide ? 0.f : 1.f / s;
+    }
+    __device__ __noinline__ uint32_t exact(float a, float b, float c, float d) const {
+        const float x[4] = {a, b, c, d};
+        uint32_t w = 0;
+        for (int i = 0; i < 4; ++i) {
+            int q = scale > 0.f ? __float2int_rn(__fdiv_rn(x[i], scale)) : 0;
+            q = q > 127 ? 127 : q < -127 ? -127 : q;
+            w |= uint32_t(q & 0xff) << (8 * i);
+        }
+        return w;
+    }
+    __device__ __forceinline__ uint32_t operator()(float a, float b, float c, float d) const {
+        const float x[4] = {a, b, c, d};
+        float f[4], off = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float t = x[i] * inv;
+            f[i] = t + 12582912.f;  // the integer in the low bits, two's complement
+            off = fmaxf(off, fabsf(t - (f[i] - 12582912.f)));
+        }
+        if (divide || off > 0.5f - 0x1p-13f) return exact(a, b, c, d);
+        const uint32_t lo = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    }
+};
 
 template <int D>
 __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int (&src)[16], int64_t block, int g, bool v,
@@ -237,70 +282,77 @@ __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int (&s
     __syncwarp();
     if (lane == 0 && (grown || anew)) *scale_at = scale;
 
-    auto again = [&](int code) -> int {  // an old code under the new scale
-        const int c = scale > 0.f ? __float2int_rn(__fdiv_rn(__fmul_rn(float(code), old), scale)) : 0;
-        return c > 127 ? 127 : c < -127 ? -127 : c;
+    const Quantizer quantize(scale);
+    // four old codes (bytes) under the new scale
+    auto again = [&](uint32_t w) -> uint32_t {
+        return quantize(__fmul_rn(float(int8_t(w)), old), __fmul_rn(float(int8_t(w >> 8)), old),
+                        __fmul_rn(float(int8_t(w >> 16)), old), __fmul_rn(float(int8_t(w >> 24)), old));
     };
     if (!v) {
-        int8_t* base = static_cast<int8_t*>(p.k_cache) + tile * 16 * D;
+        uint8_t* base = static_cast<uint8_t*>(p.k_cache) + tile * 16 * D;
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
             const int r = row_of(j);
-            char2* at_lo = reinterpret_cast<char2*>(base + r * D + lo);
-            char2* at_hi = reinterpret_cast<char2*>(base + r * D + hi);
-            if (src[r] >= 0) {
-                *at_lo = make_char2(quantize(x[j][0], scale), quantize(x[j][1], scale));
-                *at_hi = make_char2(quantize(x[j][2], scale), quantize(x[j][3], scale));
-            } else if (anew) {
-                *at_lo = make_char2(0, 0);
-                *at_hi = make_char2(0, 0);
-            } else if (grown) {
-                const char2 a = *at_lo, b = *at_hi;
-                *at_lo = make_char2(again(a.x), again(a.y));
-                *at_hi = make_char2(again(b.x), again(b.y));
-            }
+            uint16_t* at_lo = reinterpret_cast<uint16_t*>(base + r * D + lo);
+            uint16_t* at_hi = reinterpret_cast<uint16_t*>(base + r * D + hi);
+            const bool is_new = src[r] >= 0;
+            if (!is_new && !anew && !grown) continue;
+            uint32_t w = 0;
+            if (is_new) w = quantize(x[j][0], x[j][1], x[j][2], x[j][3]);
+            else if (!anew) w = again(uint32_t(*at_lo) | uint32_t(*at_hi) << 16);
+            *at_lo = uint16_t(w);
+            *at_hi = uint16_t(w >> 16);
         }
     } else {
-        // column d's bytes of the transposed tile: this lane's NR of the 16
-        int8_t* base = static_cast<int8_t*>(p.v_cache) + tile * 16 * D;
+        // column lo + e: this lane's NR of its 16 bytes
+        uint8_t* base = static_cast<uint8_t*>(p.v_cache) + tile * 16 * D + 4 * l * 16 + 8 * half;
+        uint32_t w[4][NR / 4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            int8_t* at = base + (4 * l + e) * 16 + 8 * half;
-            uint32_t w[NR / 4];
             if constexpr (NR == 16) {
-                const uint4 o = any_old && !anew ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
-                w[0] = o.x, w[1] = o.y, w[2] = o.z, w[3] = o.w;
+                const uint4 o = any_old && !anew ? *reinterpret_cast<const uint4*>(base + e * 16) : make_uint4(0, 0, 0, 0);
+                w[e][0] = o.x, w[e][1] = o.y, w[e][2] = o.z, w[e][3] = o.w;
             } else {
-                const uint2 o = any_old && !anew ? *reinterpret_cast<const uint2*>(at) : make_uint2(0, 0);
-                w[0] = o.x, w[1] = o.y;
+                const uint2 o = any_old && !anew ? *reinterpret_cast<const uint2*>(base + e * 16) : make_uint2(0, 0);
+                w[e][0] = o.x, w[e][1] = o.y;
+            }
+            if (any_old && grown && !anew) {
+#pragma unroll
+                for (int k = 0; k < NR / 4; ++k) w[e][k] = again(w[e][k]);
+            }
+        }
+        // a word of a column holds rows 2k, 2k+1, 2k+8, 2k+9 (of the lane's rows)
+#pragma unroll
+        for (int k = 0; k < NR / 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = 2 * k + (i & 1) + (i >> 1) * (NR / 2);
+                if (src[row_of(j)] < 0) continue;
+                const uint32_t c = quantize(x[j][0], x[j][1], x[j][2], x[j][3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t sel = (0x3210u & ~(0xfu << (4 * i))) | uint32_t(4 + e) << (4 * i);
+                    w[e][k] = __byte_perm(w[e][k], c, sel);
+                }
             }
 #pragma unroll
-            for (int j = 0; j < NR; ++j) {
-                const int r = row_of(j);
-                const int byte = NR == 16 ? 4 * ((j & 7) >> 1) + 2 * (j >> 3) + (j & 1)
-                                          : 4 * ((j & 3) >> 1) + 2 * (j >> 2) + (j & 1);
-                const int sh = 8 * (byte & 3);
-                int code;
-                if (src[r] >= 0) code = quantize(x[j][e], scale);
-                else if (grown) code = again(int8_t(w[byte >> 2] >> sh));
-                else continue;
-                w[byte >> 2] = (w[byte >> 2] & ~(0xffu << sh)) | (uint32_t(code & 0xff) << sh);
-            }
-            if constexpr (NR == 16) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[2], w[3]);
-            else *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (NR == 16) *reinterpret_cast<uint4*>(base + e * 16) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+            else *reinterpret_cast<uint2*>(base + e * 16) = make_uint2(w[e][0], w[e][1]);
         }
     }
 }
 
-template <int D>
+template <int D, int HP>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_i8_kernel(const __grid_constant__ RopeParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (int(blockIdx.x) >= p.kv_ctas) {  // the queries
-        constexpr int cpr = D / 16;
-        const int64_t i = (int64_t(blockIdx.x) - p.kv_ctas) * kRopeThreads + threadIdx.x;
-        const int64_t t = i / (p.Hq * cpr);
-        if (t >= p.T) return;
-        const int r = int(i - t * (p.Hq * cpr));
-        rope_rows(p, t, r / cpr, 1, r % cpr);
+        constexpr uint32_t cpr = D / 16;
+        const uint32_t per_token = (p.Hq + HP - 1) / HP * cpr;
+        const uint32_t i = (blockIdx.x - p.kv_ctas) * uint32_t(kRopeThreads) + threadIdx.x;
+        const uint32_t t = i / per_token, r = i - t * per_token;
+        if (t < uint32_t(p.T)) rope_rows<HP>(p, int(t), int(r / cpr) * HP, p.Hq, int(r % cpr));
         return;
     }
     __shared__ int src[16];    // the call's token of each row of the block, -1: none
@@ -321,6 +373,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_i8_kernel(const __gr
     if (threadIdx.x < 16) src[threadIdx.x] = -1;
     if (threadIdx.x == 0) not_first = 0;
     __syncthreads();
+#pragma unroll 8
     for (int u = threadIdx.x; u < p.T; u += kRopeThreads) {
         const int32_t s = __ldg(p.slot_mapping + u);
         if (s < 0 || s / 16 != block) continue;

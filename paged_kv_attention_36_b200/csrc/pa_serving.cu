@@ -289,26 +289,35 @@ pa_status prepare_append(const Append& a, bool i8, pa::RopeParams& p) {
     return PA_OK;
 }
 
+// Rows a thread takes: four share one read of the angles once there are enough
+// threads for every SM without (2048 each).
+bool rows_in_fours(int64_t rows, int D, int sms) { return rows * (D / 16) >= int64_t(4) * 2048 * sms; }
+
 template <int HP>
 pa_status launch_rope(const pa::RopeParams& p, cudaStream_t s) {
     const int64_t items = int64_t(p.T) * ((p.Hq + 2 * p.Hkv + HP - 1) / HP) * (p.D / 16);
-    const int64_t ctas = (items + pa::kRopeThreads - 1) / pa::kRopeThreads;
+    if (items >= int64_t(1) << 32) return PA_ERR_SHAPE;
+    const unsigned ctas = unsigned((items + pa::kRopeThreads - 1) / pa::kRopeThreads);
+    return launch_dependent(pa::rope_append_kernel<HP>, dim3(ctas), pa::kRopeThreads, 0, s, p);
+}
+
+template <int D, int HP>
+pa_status launch_rope_i8(pa::RopeParams& p, cudaStream_t s) {
+    const int64_t items = int64_t(p.T) * ((p.Hq + HP - 1) / HP) * (D / 16);
+    if (items >= int64_t(1) << 32) return PA_ERR_SHAPE;
+    p.kv_ctas = p.T;
+    const int64_t ctas = p.T + (items + pa::kRopeThreads - 1) / pa::kRopeThreads;
     if (ctas > 0x7fffffff) return PA_ERR_SHAPE;
-    pa::rope_append_kernel<HP><<<unsigned(ctas), pa::kRopeThreads, 0, s>>>(p);
-    return launched();
+    return launch_dependent(pa::rope_append_i8_kernel<D, HP>, dim3(unsigned(ctas)), pa::kRopeThreads, 0, s, p);
 }
 
 pa_status append_i8(const Append& a, cudaStream_t s) {
     pa::RopeParams p;
     const pa_status st = prepare_append(a, true, p);
     if (st != PA_OK || p.T == 0) return st;
-    const int64_t q_items = int64_t(p.T) * p.Hq * (p.D / 16);
-    const int64_t ctas = p.T + (q_items + pa::kRopeThreads - 1) / pa::kRopeThreads;
-    if (ctas > 0x7fffffff) return PA_ERR_SHAPE;
-    p.kv_ctas = p.T;
-    if (p.D == 64) pa::rope_append_i8_kernel<64><<<unsigned(ctas), pa::kRopeThreads, 0, s>>>(p);
-    else pa::rope_append_i8_kernel<128><<<unsigned(ctas), pa::kRopeThreads, 0, s>>>(p);
-    return launched();
+    const bool fours = rows_in_fours(int64_t(p.T) * p.Hq, p.D, sm_count());
+    if (p.D == 64) return fours ? launch_rope_i8<64, 4>(p, s) : launch_rope_i8<64, 1>(p, s);
+    return fours ? launch_rope_i8<128, 4>(p, s) : launch_rope_i8<128, 1>(p, s);
 }
 
 }  // namespace
@@ -379,7 +388,8 @@ pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k_new, int
                                                num_tokens, q_out, k_cache, v_cache, nullptr, nullptr, dims},
                                         false, p);
     if (st != PA_OK || p.T == 0) return st;
-    return launch_rope<1>(p, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return rows_in_fours(int64_t(p.T) * (p.Hq + 2 * p.Hkv), p.D, sm_count()) ? launch_rope<4>(p, s) : launch_rope<1>(p, s);
 }
 
 pa_status pa_rope_append_i8(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
