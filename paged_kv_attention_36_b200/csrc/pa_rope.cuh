@@ -32,6 +32,7 @@ struct RopeParams {
     int32_t T, Hq, Hkv, D, bs, NB;
     int32_t max_position, rd, interleaved;
     int32_t kv_ctas;              // 8-bit: the first kv_ctas CTAs take the blocks, the others the queries
+    int32_t tokens_per_cta;       // 8-bit: tokens whose blocks a CTA looks at, at most 32
 };
 
 constexpr int kRopeThreads = 256;
@@ -151,7 +152,7 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, int t, int h0, in
 
 // One thread per chunk pair of HP consecutive rows of a token.
 template <int HP>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_append_kernel(const __grid_constant__ RopeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t heads = p.Hq + 2 * p.Hkv, cpr = p.D / 16, per_token = (heads + HP - 1) / HP * cpr;
@@ -183,17 +184,21 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const __grid_
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 // round(x / scale) of four values as bytes, the division and the rounding IEEE
-// fp32 (ties to even).  x * (1/scale) is off by at most 2 ulp of the quotient,
-// so unless it comes within 2^-13 of a tie it rounds to the same code; those
-// few, and scales whose reciprocal leaves the normal range, are divided.
+// fp32 (ties to even).  t = x * (1/scale) is within 2^-15 of the quotient
+// (|t| <= 127 and three roundings), so away from ties it rounds to the same
+// code.  Near one, at mid = n +- 1/2: r = x - mid * scale is exact in one fma
+// (both sides agree in all but their last bits), and the divided quotient
+// rounds to mid itself iff |r| <= scale * half an ulp of mid; then the even
+// neighbour is taken, else the side of mid that r says.  Scales whose
+// reciprocal leaves the normal range divide.
 struct Quantizer {
     float scale, inv;
     bool divide;
     __device__ __forceinline__ explicit Quantizer(float s) : scale(s) {
-        divide = !(s > 1e-35f && s < 1e35f);
+        divide = !(s > 1e-30f && s < 1e30f);
         inv = divide ? 0.f : 1.f / s;
     }
-    __device__ __noinline__ uint32_t exact(float a, float b, float c, float d) const {
+    __device__ __noinline__ uint32_t divided(float a, float b, float c, float d) const {
         const float x[4] = {a, b, c, d};
         uint32_t w = 0;
         for (int i = 0; i < 4; ++i) {
@@ -205,25 +210,39 @@ struct Quantizer {
     }
     __device__ __forceinline__ uint32_t operator()(float a, float b, float c, float d) const {
         const float x[4] = {a, b, c, d};
-        float f[4], off = 0.f;
+        float n[4], off[4], worst = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float t = x[i] * inv;
-            f[i] = t + 12582912.f;  // the integer in the low bits, two's complement
-            off = fmaxf(off, fabsf(t - (f[i] - 12582912.f)));
+            n[i] = t + 12582912.f - 12582912.f;  // rint(t)
+            off[i] = t - n[i];
+            worst = fmaxf(worst, fabsf(off[i]));
         }
-        if (divide || off > 0.5f - 0x1p-13f) return exact(a, b, c, d);
-        const uint32_t lo = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0040);
-        const uint32_t hi = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0040);
+        if (worst > 0.5f - 0x1p-15f) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (fabsf(off[i]) <= 0.5f - 0x1p-15f) continue;
+                const float way = off[i] < 0.f ? -1.f : 1.f, mid = n[i] + 0.5f * way;
+                const float r = fmaf(-mid, scale, x[i]);
+                // half an ulp of mid: 2^(exponent - 24)
+                const float half = __uint_as_float((__float_as_uint(mid) & 0x7f800000u) - (24u << 23));
+                const bool tie = fabsf(r) <= scale * half;
+                const bool odd = (__float_as_uint(n[i] + 12582912.f) & 1u) != 0;
+                if (tie ? odd : r * way > 0.f) n[i] += way;
+            }
+        }
+        // the integers in the low bits of n + 12582912, two's complement
+        const uint32_t lo = __byte_perm(__float_as_uint(n[0] + 12582912.f), __float_as_uint(n[1] + 12582912.f), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(n[2] + 12582912.f), __float_as_uint(n[3] + 12582912.f), 0x0040);
         return __byte_perm(lo, hi, 0x5410);
     }
 };
 
 template <int D>
-__device__ __forceinline__ void quantize_tile(const RopeParams& p, const int (&src)[16], int64_t block, int g, bool v,
-                                              int lane) {
+__device__ __forceinline__ void quantize_tile(const RopeParams& p, const int* src, int64_t block, int g, bool v,
+                                              uint8_t* stage, int lane) {
     constexpr int LPR = D / 4;        // lanes per row
-    constexpr int NR = 16 * LPR / 32;  // rows a lane holds: 16, or 8 at head_dim 64
+    constexpr int NR = 16 * LPR / 32;  // rows a lane has: 16, or 8 at head_dim 64
     const int half = lane / LPR, l = lane % LPR;
     // this lane's four columns: lo, lo+1, hi, hi+1
     const int rd = v ? 0 : p.rd;
@@ -236,46 +255,60 @@ __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int (&s
     // rows in the order of the V tile's bytes: at head_dim 64 the first half
     // warp has tokens 0-3 and 8-11, the second 4-7 and 12-15
     auto row_of = [&](int j) -> int { return NR == 16 ? j : (j & 3) + ((j >> 2) << 3) + 4 * half; };
-
-    float x[NR][4];
-    uint32_t top = 0;
-    bool any_old = false;  // rows of the block that the call does not write
+    const __nv_bfloat16* rows = (v ? p.v_new : p.k_new) + int64_t(g) * D;
+    const int64_t stride = v ? p.v_stride : p.k_stride;
+    // All of the call's rows of this tile at once into the warp's staging
+    // area (row by row from global memory, each group of rows waited a memory
+    // latency, twice).
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < NR; ++j) {
-        const int t = src[row_of(j)];
-        x[j][0] = x[j][1] = x[j][2] = x[j][3] = 0.f;
-        if (t < 0) {
-            any_old = true;
-            continue;
-        }
-        const __nv_bfloat16* row = v ? p.v_new + t * p.v_stride + int64_t(g) * D : p.k_new + t * p.k_stride + int64_t(g) * D;
-        const float2 a = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(row + lo));
-        const float2 b = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(row + hi));
-        x[j][0] = a.x;
-        x[j][1] = a.y;
-        x[j][2] = b.x;
-        x[j][3] = b.y;
+    for (int x = lane; x < 16 * (D / 8); x += 32) {
+        const int t = src[x / (D / 8)];
+        if (t >= 0) cp_async16(stage + x * 16, rows + t * stride + x % (D / 8) * 8);
+    }
+    cp_async_commit();
+    const int64_t tile = block * p.Hkv + g;
+    float* scale_at = (v ? p.v_scale : p.k_scale) + tile;
+    const bool anew = src[0] >= 0;
+    const float old = anew ? 0.f : *scale_at;
+    cp_async_wait_all();
+    __syncwarp();
+    // the lane's four values of row r (token t), turned
+    auto load = [&](int r, int t, float (&x)[4]) {
+        const uint8_t* row = stage + r * D * 2;
+        const float2 a = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(row + lo * 2));
+        const float2 b = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(row + hi * 2));
+        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
         if (rotate) {
             const float* cs = angles(p, t, false) + 2 * l;
             const float2 c = __ldg(reinterpret_cast<const float2*>(cs));
             const float2 s = __ldg(reinterpret_cast<const float2*>(cs + rd / 2));
             if (p.interleaved) {
-                turn(x[j][0], x[j][1], c.x, s.x);
-                turn(x[j][2], x[j][3], c.y, s.y);
+                turn(x[0], x[1], c.x, s.x);
+                turn(x[2], x[3], c.y, s.y);
             } else {
-                turn(x[j][0], x[j][2], c.x, s.x);
-                turn(x[j][1], x[j][3], c.y, s.y);
+                turn(x[0], x[2], c.x, s.x);
+                turn(x[1], x[3], c.y, s.y);
             }
         }
+    };
+
+    uint32_t top = 0;
+    bool any_old = false;  // rows of the block that the call does not write
+#pragma unroll 4
+    for (int j = 0; j < NR; ++j) {
+        const int t = src[row_of(j)];
+        if (t < 0) {
+            any_old = true;
+            continue;
+        }
+        float x[4];
+        load(row_of(j), t, x);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, abs_bits(x[j][e]));
+        for (int e = 0; e < 4; ++e) top = max(top, abs_bits(x[e]));
     }
     top = __reduce_max_sync(0xffffffffu, top);
 
-    const int64_t tile = block * p.Hkv + g;
-    float* scale_at = (v ? p.v_scale : p.k_scale) + tile;
-    const bool anew = src[0] >= 0;
-    const float old = anew ? 0.f : *scale_at;
     const float need = __fdiv_rn(__uint_as_float(top), 127.f);
     const float scale = need <= old || old != old ? old : need;  // NaN stays
     const bool grown = !(scale <= old);
@@ -283,23 +316,30 @@ __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int (&s
     if (lane == 0 && (grown || anew)) *scale_at = scale;
 
     const Quantizer quantize(scale);
+    auto codes = [&](float a, float b, float c, float d) {
+        return quantize.divide ? quantize.divided(a, b, c, d) : quantize(a, b, c, d);
+    };
     // four old codes (bytes) under the new scale
     auto again = [&](uint32_t w) -> uint32_t {
-        return quantize(__fmul_rn(float(int8_t(w)), old), __fmul_rn(float(int8_t(w >> 8)), old),
-                        __fmul_rn(float(int8_t(w >> 16)), old), __fmul_rn(float(int8_t(w >> 24)), old));
+        return codes(__fmul_rn(float(int8_t(w)), old), __fmul_rn(float(int8_t(w >> 8)), old),
+                     __fmul_rn(float(int8_t(w >> 16)), old), __fmul_rn(float(int8_t(w >> 24)), old));
     };
     if (!v) {
         uint8_t* base = static_cast<uint8_t*>(p.k_cache) + tile * 16 * D;
-#pragma unroll
+#pragma unroll 4
         for (int j = 0; j < NR; ++j) {
-            const int r = row_of(j);
+            const int r = row_of(j), t = src[r];
             uint16_t* at_lo = reinterpret_cast<uint16_t*>(base + r * D + lo);
             uint16_t* at_hi = reinterpret_cast<uint16_t*>(base + r * D + hi);
-            const bool is_new = src[r] >= 0;
-            if (!is_new && !anew && !grown) continue;
+            if (t < 0 && !anew && !grown) continue;
             uint32_t w = 0;
-            if (is_new) w = quantize(x[j][0], x[j][1], x[j][2], x[j][3]);
-            else if (!anew) w = again(uint32_t(*at_lo) | uint32_t(*at_hi) << 16);
+            if (t >= 0) {
+                float x[4];
+                load(r, t, x);
+                w = codes(x[0], x[1], x[2], x[3]);
+            } else if (!anew) {
+                w = again(uint32_t(*at_lo) | uint32_t(*at_hi) << 16);
+            }
             *at_lo = uint16_t(w);
             *at_hi = uint16_t(w >> 16);
         }
@@ -326,9 +366,11 @@ __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int (&s
         for (int k = 0; k < NR / 4; ++k)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int j = 2 * k + (i & 1) + (i >> 1) * (NR / 2);
-                if (src[row_of(j)] < 0) continue;
-                const uint32_t c = quantize(x[j][0], x[j][1], x[j][2], x[j][3]);
+                const int r = row_of(2 * k + (i & 1) + (i >> 1) * (NR / 2)), t = src[r];
+                if (t < 0) continue;
+                float x[4];
+                load(r, t, x);
+                const uint32_t c = codes(x[0], x[1], x[2], x[3]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t sel = (0x3210u & ~(0xfu << (4 * i))) | uint32_t(4 + e) << (4 * i);
@@ -344,7 +386,7 @@ __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int (&s
 }
 
 template <int D, int HP>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_i8_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_append_i8_kernel(const __grid_constant__ RopeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (int(blockIdx.x) >= p.kv_ctas) {  // the queries
@@ -355,38 +397,41 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_i8_kernel(const __gr
         if (t < uint32_t(p.T)) rope_rows<HP>(p, int(t), int(r / cpr) * HP, p.Hq, int(r % cpr));
         return;
     }
+    __shared__ __align__(16) uint8_t stages[kRopeThreads / 32][16 * D * 2];
     __shared__ int src[16];    // the call's token of each row of the block, -1: none
     __shared__ int not_first;  // another token of the block comes before
-    const int t = blockIdx.x;
-    const int32_t slot = __ldg(p.slot_mapping + t);
-    if (slot < 0) return;
-    const int32_t block = slot / 16;
-    if (block >= p.NB) {
-        if (threadIdx.x == 0) raise_error(PA_DEVERR_SLOT);
-        return;
+    // This CTA's tokens (at most 32); those right behind a token of their own
+    // block cannot be its first.  Every warp sees the same mask.
+    const int lane = threadIdx.x & 31, t0 = blockIdx.x * p.tokens_per_cta;
+    const bool here = lane < p.tokens_per_cta && t0 + lane < p.T;
+    const int32_t my_slot = here ? __ldg(p.slot_mapping + t0 + lane) : -1;
+    const int32_t before = here && t0 + lane > 0 ? __ldg(p.slot_mapping + t0 + lane - 1) : -1;
+    bool candidate = my_slot >= 0;
+    if (candidate && my_slot / 16 >= p.NB) {
+        if (threadIdx.x < 32) raise_error(PA_DEVERR_SLOT);
+        candidate = false;
     }
-    if (p.rd > 0) angles(p, t, threadIdx.x == 0);  // reports a position without a table row
-    if (t > 0) {
-        const int32_t before = __ldg(p.slot_mapping + t - 1);
-        if (before >= 0 && before / 16 == block) return;
-    }
-    if (threadIdx.x < 16) src[threadIdx.x] = -1;
-    if (threadIdx.x == 0) not_first = 0;
-    __syncthreads();
+    if (candidate && p.rd > 0) angles(p, t0 + lane, threadIdx.x < 32);  // reports a position without a table row
+    if (before >= 0 && before / 16 == my_slot / 16) candidate = false;
+    for (unsigned todo = __ballot_sync(0xffffffffu, candidate); todo; todo &= todo - 1) {
+        const int i = __ffs(todo) - 1, t = t0 + i;
+        const int32_t block = __shfl_sync(0xffffffffu, my_slot, i) / 16;
+        __syncthreads();  // the last block's src has been read
+        if (threadIdx.x < 16) src[threadIdx.x] = -1;
+        if (threadIdx.x == 0) not_first = 0;
+        __syncthreads();
 #pragma unroll 8
-    for (int u = threadIdx.x; u < p.T; u += kRopeThreads) {
-        const int32_t s = __ldg(p.slot_mapping + u);
-        if (s < 0 || s / 16 != block) continue;
-        if (u < t) not_first = 1;
-        atomicMax(&src[s & 15], u);  // of two tokens in one slot the later lands
+        for (int u = threadIdx.x; u < p.T; u += kRopeThreads) {
+            const int32_t s = __ldg(p.slot_mapping + u);
+            if (s < 0 || s / 16 != block) continue;
+            if (u < t) not_first = 1;
+            atomicMax(&src[s & 15], u);  // of two tokens in one slot the later lands
+        }
+        __syncthreads();
+        if (not_first) continue;
+        for (int x = threadIdx.x >> 5; x < 2 * p.Hkv; x += kRopeThreads / 32)
+            quantize_tile<D>(p, src, block, x >> 1, x & 1, stages[threadIdx.x >> 5], lane);
     }
-    __syncthreads();
-    if (not_first) return;
-    int rows[16];
-#pragma unroll
-    for (int r = 0; r < 16; ++r) rows[r] = src[r];
-    for (int x = threadIdx.x >> 5; x < 2 * p.Hkv; x += kRopeThreads / 32)
-        quantize_tile<D>(p, rows, block, x >> 1, x & 1, threadIdx.x & 31);
 }
 
 }  // namespace pa

@@ -305,8 +305,12 @@ template <int D, int HP>
 pa_status launch_rope_i8(pa::RopeParams& p, cudaStream_t s) {
     const int64_t items = int64_t(p.T) * ((p.Hq + HP - 1) / HP) * (D / 16);
     if (items >= int64_t(1) << 32) return PA_ERR_SHAPE;
-    p.kv_ctas = p.T;
-    const int64_t ctas = p.T + (items + pa::kRopeThreads - 1) / pa::kRopeThreads;
+    // a decode step's tokens have a block each and a CTA each; of a long call's
+    // tokens few are their block's first, and a CTA looks at up to 16
+    const int sms = sm_count();
+    p.tokens_per_cta = p.T <= 4 * sms ? 1 : p.T / (4 * sms) < 16 ? p.T / (4 * sms) : 16;
+    p.kv_ctas = (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
+    const int64_t ctas = p.kv_ctas + (items + pa::kRopeThreads - 1) / pa::kRopeThreads;
     if (ctas > 0x7fffffff) return PA_ERR_SHAPE;
     return launch_dependent(pa::rope_append_i8_kernel<D, HP>, dim3(unsigned(ctas)), pa::kRopeThreads, 0, s, p);
 }
