@@ -13,6 +13,7 @@
 
 #include "pa_append.cuh"
 #include "pa_device.cuh"
+#include "pa_tcgen05.cuh"  // packed fp32 pairs
 
 namespace pa {
 
@@ -33,6 +34,7 @@ struct RopeParams {
     int32_t max_position, rd, interleaved;
     int32_t kv_ctas;              // 8-bit: the first kv_ctas CTAs take the blocks, the others the queries
     int32_t tokens_per_cta;       // 8-bit: tokens whose blocks a CTA looks at, at most 32
+    int32_t parts;                // 8-bit: CTAs that share the tiles of the same tokens
 };
 
 constexpr int kRopeThreads = 256;
@@ -198,7 +200,7 @@ struct Quantizer {
         divide = !(s > 1e-30f && s < 1e30f);
         inv = divide ? 0.f : 1.f / s;
     }
-    __device__ __noinline__ uint32_t divided(float a, float b, float c, float d) const {
+    static __device__ __noinline__ uint32_t divided(float scale, float a, float b, float c, float d) {
         const float x[4] = {a, b, c, d};
         uint32_t w = 0;
         for (int i = 0; i < 4; ++i) {
@@ -208,39 +210,58 @@ struct Quantizer {
         }
         return w;
     }
-    __device__ __forceinline__ uint32_t operator()(float a, float b, float c, float d) const {
-        const float x[4] = {a, b, c, d};
-        float n[4], off[4], worst = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float t = x[i] * inv;
-            n[i] = t + 12582912.f - 12582912.f;  // rint(t)
-            off[i] = t - n[i];
-            worst = fmaxf(worst, fabsf(off[i]));
-        }
+    // values (x01, x23) as packed pairs
+    __device__ __forceinline__ uint32_t operator()(uint64_t x01, uint64_t x23) const {
+        const uint64_t up = f2_pack(12582912.f, 12582912.f), down = f2_pack(-12582912.f, -12582912.f);
+        const uint64_t by = f2_pack(inv, inv), minus = f2_pack(-1.f, -1.f);
+        const uint64_t t01 = f2_mul(x01, by), t23 = f2_mul(x23, by);
+        const uint64_t r01 = f2_add(t01, up), r23 = f2_add(t23, up);  // the integers in the low bits
+        const uint64_t o01 = f2_fma(f2_add(r01, down), minus, t01), o23 = f2_fma(f2_add(r23, down), minus, t23);
+        float r[4], off[4];
+        f2_unpack(r01, r[0], r[1]);
+        f2_unpack(r23, r[2], r[3]);
+        f2_unpack(o01, off[0], off[1]);
+        f2_unpack(o23, off[2], off[3]);
+        const float worst = fmaxf(fmax3(fabsf(off[0]), fabsf(off[1]), fabsf(off[2])), fabsf(off[3]));
         if (worst > 0.5f - 0x1p-15f) {
+            float x[4];
+            f2_unpack(x01, x[0], x[1]);
+            f2_unpack(x23, x[2], x[3]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (fabsf(off[i]) <= 0.5f - 0x1p-15f) continue;
-                const float way = off[i] < 0.f ? -1.f : 1.f, mid = n[i] + 0.5f * way;
-                const float r = fmaf(-mid, scale, x[i]);
+                const float way = off[i] < 0.f ? -1.f : 1.f, mid = r[i] - 12582912.f + 0.5f * way;
+                const float rest = fmaf(-mid, scale, x[i]);
                 // half an ulp of mid: 2^(exponent - 24)
                 const float half = __uint_as_float((__float_as_uint(mid) & 0x7f800000u) - (24u << 23));
-                const bool tie = fabsf(r) <= scale * half;
-                const bool odd = (__float_as_uint(n[i] + 12582912.f) & 1u) != 0;
-                if (tie ? odd : r * way > 0.f) n[i] += way;
+                const bool tie = fabsf(rest) <= scale * half, odd = (__float_as_uint(r[i]) & 1u) != 0;
+                if (tie ? odd : rest * way > 0.f) r[i] += way;
             }
         }
-        // the integers in the low bits of n + 12582912, two's complement
-        const uint32_t lo = __byte_perm(__float_as_uint(n[0] + 12582912.f), __float_as_uint(n[1] + 12582912.f), 0x0040);
-        const uint32_t hi = __byte_perm(__float_as_uint(n[2] + 12582912.f), __float_as_uint(n[3] + 12582912.f), 0x0040);
+        const uint32_t lo = __byte_perm(__float_as_uint(r[0]), __float_as_uint(r[1]), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(r[2]), __float_as_uint(r[3]), 0x0040);
         return __byte_perm(lo, hi, 0x5410);
     }
 };
 
+// Starts the copy of all of the call's rows of a tile (kv head g, K or V) into
+// `stage` ([16][D] bf16); rows the call does not have are left alone.
+template <int D>
+__device__ __forceinline__ void stage_rows(const RopeParams& p, const int* src, int g, bool v, uint8_t* stage, int lane) {
+    const __nv_bfloat16* rows = (v ? p.v_new : p.k_new) + int64_t(g) * D;
+    const int64_t stride = v ? p.v_stride : p.k_stride;
+#pragma unroll
+    for (int x = lane; x < 16 * (D / 8); x += 32) {
+        const int t = src[x / (D / 8)];
+        if (t >= 0) cp_async16(stage + x * 16, rows + t * stride + x % (D / 8) * 8);
+    }
+}
+
+// `stage`: the tile's rows (stage_rows), `table`: the angles of the block's
+// rows, [16][rd] as in cos_sin.
 template <int D>
 __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int* src, int64_t block, int g, bool v,
-                                              uint8_t* stage, int lane) {
+                                              const uint8_t* stage, const float* table, int lane) {
     constexpr int LPR = D / 4;        // lanes per row
     constexpr int NR = 16 * LPR / 32;  // rows a lane has: 16, or 8 at head_dim 64
     const int half = lane / LPR, l = lane % LPR;
@@ -255,58 +276,47 @@ __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int* sr
     // rows in the order of the V tile's bytes: at head_dim 64 the first half
     // warp has tokens 0-3 and 8-11, the second 4-7 and 12-15
     auto row_of = [&](int j) -> int { return NR == 16 ? j : (j & 3) + ((j >> 2) << 3) + 4 * half; };
-    const __nv_bfloat16* rows = (v ? p.v_new : p.k_new) + int64_t(g) * D;
-    const int64_t stride = v ? p.v_stride : p.k_stride;
-    // All of the call's rows of this tile at once into the warp's staging
-    // area (row by row from global memory, each group of rows waited a memory
-    // latency, twice).
-    __syncwarp();
-#pragma unroll
-    for (int x = lane; x < 16 * (D / 8); x += 32) {
-        const int t = src[x / (D / 8)];
-        if (t >= 0) cp_async16(stage + x * 16, rows + t * stride + x % (D / 8) * 8);
-    }
-    cp_async_commit();
     const int64_t tile = block * p.Hkv + g;
     float* scale_at = (v ? p.v_scale : p.k_scale) + tile;
     const bool anew = src[0] >= 0;
     const float old = anew ? 0.f : *scale_at;
-    cp_async_wait_all();
-    __syncwarp();
-    // the lane's four values of row r (token t), turned
-    auto load = [&](int r, int t, float (&x)[4]) {
+    // the lane's four values of row r, turned, as (lo, lo+1) and (hi, hi+1)
+    auto load = [&](int r, uint64_t& x01, uint64_t& x23) {
         const uint8_t* row = stage + r * D * 2;
-        const float2 a = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(row + lo * 2));
-        const float2 b = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(row + hi * 2));
-        x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+        float2 a = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(row + lo * 2));
+        float2 b = bf16x2_to_float2(*reinterpret_cast<const uint32_t*>(row + hi * 2));
         if (rotate) {
-            const float* cs = angles(p, t, false) + 2 * l;
-            const float2 c = __ldg(reinterpret_cast<const float2*>(cs));
-            const float2 s = __ldg(reinterpret_cast<const float2*>(cs + rd / 2));
+            const float2 c = *reinterpret_cast<const float2*>(table + r * rd + 2 * l);
+            const float2 s = *reinterpret_cast<const float2*>(table + r * rd + rd / 2 + 2 * l);
             if (p.interleaved) {
-                turn(x[0], x[1], c.x, s.x);
-                turn(x[2], x[3], c.y, s.y);
+                turn(a.x, a.y, c.x, s.x);
+                turn(b.x, b.y, c.y, s.y);
             } else {
-                turn(x[0], x[2], c.x, s.x);
-                turn(x[1], x[3], c.y, s.y);
+                turn(a.x, b.x, c.x, s.x);
+                turn(a.y, b.y, c.y, s.y);
             }
         }
+        x01 = f2_pack(a.x, a.y);
+        x23 = f2_pack(b.x, b.y);
     };
 
+    // the lane's rows that the call has, as bits
+    const uint32_t have = [&] {
+        const uint32_t all = __ballot_sync(0xffffffffu, l < NR && src[row_of(l < NR ? l : 0)] >= 0);
+        return NR == 16 ? all & 0xffffu : all >> (16 * half) & 0xffu;
+    }();
     uint32_t top = 0;
-    bool any_old = false;  // rows of the block that the call does not write
-#pragma unroll 4
-    for (int j = 0; j < NR; ++j) {
-        const int t = src[row_of(j)];
-        if (t < 0) {
-            any_old = true;
-            continue;
-        }
+#pragma unroll 1
+    for (uint32_t left = have; left; left &= left - 1) {
+        uint64_t x01, x23;
+        load(row_of(__ffs(left) - 1), x01, x23);
         float x[4];
-        load(row_of(j), t, x);
+        f2_unpack(x01, x[0], x[1]);
+        f2_unpack(x23, x[2], x[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = max(top, abs_bits(x[e]));
     }
+    __syncwarp();
     top = __reduce_max_sync(0xffffffffu, top);
 
     const float need = __fdiv_rn(__uint_as_float(top), 127.f);
@@ -315,72 +325,101 @@ __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int* sr
     __syncwarp();
     if (lane == 0 && (grown || anew)) *scale_at = scale;
 
+    // The codes of the lane's four columns of row r.  The loops below are
+    // rolled around one copy of this.
     const Quantizer quantize(scale);
-    auto codes = [&](float a, float b, float c, float d) {
-        return quantize.divide ? quantize.divided(a, b, c, d) : quantize(a, b, c, d);
+    auto codes = [&](uint64_t x01, uint64_t x23) -> uint32_t {
+        if (!quantize.divide) return quantize(x01, x23);
+        float x[4];
+        f2_unpack(x01, x[0], x[1]);
+        f2_unpack(x23, x[2], x[3]);
+        return Quantizer::divided(scale, x[0], x[1], x[2], x[3]);
     };
-    // four old codes (bytes) under the new scale
-    auto again = [&](uint32_t w) -> uint32_t {
-        return codes(__fmul_rn(float(int8_t(w)), old), __fmul_rn(float(int8_t(w >> 8)), old),
-                     __fmul_rn(float(int8_t(w >> 16)), old), __fmul_rn(float(int8_t(w >> 24)), old));
+    auto row_codes = [&](int r) -> uint32_t {
+        uint64_t x01, x23;
+        load(r, x01, x23);
+        return codes(x01, x23);
     };
+    // four old codes under the new scale
+    auto again = [&](uint32_t kept) -> uint32_t {
+        return codes(f2_pack(__fmul_rn(float(int8_t(kept)), old), __fmul_rn(float(int8_t(kept >> 8)), old)),
+                     f2_pack(__fmul_rn(float(int8_t(kept >> 16)), old), __fmul_rn(float(int8_t(kept >> 24)), old)));
+    };
+    uint8_t* base = static_cast<uint8_t*>(v ? p.v_cache : p.k_cache) + tile * 16 * D;
+    if (!anew && !grown) {
+        // only the new rows change
+#pragma unroll 1
+        for (uint32_t left = have; left; left &= left - 1) {
+            const int r = row_of(__ffs(left) - 1);
+            const uint32_t w = row_codes(r);
+            if (!v) {
+                *reinterpret_cast<uint16_t*>(base + r * D + lo) = uint16_t(w);
+                *reinterpret_cast<uint16_t*>(base + r * D + hi) = uint16_t(w >> 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) base[(4 * l + e) * 16 + vt_position(r)] = uint8_t(w >> (8 * e));
+            }
+        }
+        return;
+    }
     if (!v) {
-        uint8_t* base = static_cast<uint8_t*>(p.k_cache) + tile * 16 * D;
-#pragma unroll 4
+#pragma unroll 1
         for (int j = 0; j < NR; ++j) {
-            const int r = row_of(j), t = src[r];
+            const int r = row_of(j);
             uint16_t* at_lo = reinterpret_cast<uint16_t*>(base + r * D + lo);
             uint16_t* at_hi = reinterpret_cast<uint16_t*>(base + r * D + hi);
-            if (t < 0 && !anew && !grown) continue;
-            uint32_t w = 0;
-            if (t >= 0) {
-                float x[4];
-                load(r, t, x);
-                w = codes(x[0], x[1], x[2], x[3]);
-            } else if (!anew) {
-                w = again(uint32_t(*at_lo) | uint32_t(*at_hi) << 16);
-            }
+            const uint32_t w = have >> j & 1 ? row_codes(r)
+                               : anew        ? 0u
+                                             : again(uint32_t(*at_lo) | uint32_t(*at_hi) << 16);
             *at_lo = uint16_t(w);
             *at_hi = uint16_t(w >> 16);
         }
     } else {
-        // column lo + e: this lane's NR of its 16 bytes
-        uint8_t* base = static_cast<uint8_t*>(p.v_cache) + tile * 16 * D + 4 * l * 16 + 8 * half;
-        uint32_t w[4][NR / 4];
+        // column lo + e: this lane's NR of its 16 bytes.  Word k of a column
+        // holds the lane's rows 2k, 2k+1, 2k + NR/2, 2k+1 + NR/2; the words
+        // move through the registers so that the loop's body names only w[.][0].
+        constexpr int NW = NR / 4;
+        uint8_t* at = base + 4 * l * 16 + 8 * half;
+        uint32_t w[4][NW];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if constexpr (NR == 16) {
-                const uint4 o = any_old && !anew ? *reinterpret_cast<const uint4*>(base + e * 16) : make_uint4(0, 0, 0, 0);
+                const uint4 o = anew ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4*>(at + e * 16);
                 w[e][0] = o.x, w[e][1] = o.y, w[e][2] = o.z, w[e][3] = o.w;
             } else {
-                const uint2 o = any_old && !anew ? *reinterpret_cast<const uint2*>(base + e * 16) : make_uint2(0, 0);
+                const uint2 o = anew ? make_uint2(0, 0) : *reinterpret_cast<const uint2*>(at + e * 16);
                 w[e][0] = o.x, w[e][1] = o.y;
             }
-            if (any_old && grown && !anew) {
+        }
+#pragma unroll 1
+        for (int k = 0; k < NW; ++k) {
+            uint32_t c[4] = {0u, 0u, 0u, 0u};  // the codes of four rows, a row each
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                const int j = 2 * k + (i & 1) + (i >> 1) * (NR / 2);
+                const uint32_t pick = 0x40u + 0x11u * uint32_t(i);  // byte i of each word
+                c[0] = c[1], c[1] = c[2], c[2] = c[3];
+                c[3] = have >> j & 1 ? row_codes(row_of(j))
+                       : anew        ? 0u
+                                     : again(__byte_perm(__byte_perm(w[0][0], w[1][0], pick),
+                                                         __byte_perm(w[2][0], w[3][0], pick), 0x5410));
+            }
+            // rows to columns: four 4-byte rows become four 4-byte columns
+            const uint32_t a = __byte_perm(c[0], c[1], 0x5140), b = __byte_perm(c[2], c[3], 0x5140);
+            const uint32_t d = __byte_perm(c[0], c[1], 0x7362), f = __byte_perm(c[2], c[3], 0x7362);
+            const uint32_t n[4] = {__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632), __byte_perm(d, f, 0x5410),
+                                   __byte_perm(d, f, 0x7632)};
 #pragma unroll
-                for (int k = 0; k < NR / 4; ++k) w[e][k] = again(w[e][k]);
+            for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int i = 0; i + 1 < NW; ++i) w[e][i] = w[e][i + 1];
+                w[e][NW - 1] = n[e];
             }
         }
-        // a word of a column holds rows 2k, 2k+1, 2k+8, 2k+9 (of the lane's rows)
-#pragma unroll
-        for (int k = 0; k < NR / 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = row_of(2 * k + (i & 1) + (i >> 1) * (NR / 2)), t = src[r];
-                if (t < 0) continue;
-                float x[4];
-                load(r, t, x);
-                const uint32_t c = codes(x[0], x[1], x[2], x[3]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t sel = (0x3210u & ~(0xfu << (4 * i))) | uint32_t(4 + e) << (4 * i);
-                    w[e][k] = __byte_perm(w[e][k], c, sel);
-                }
-            }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            if constexpr (NR == 16) *reinterpret_cast<uint4*>(base + e * 16) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
-            else *reinterpret_cast<uint2*>(base + e * 16) = make_uint2(w[e][0], w[e][1]);
+            if constexpr (NR == 16) *reinterpret_cast<uint4*>(at + e * 16) = make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
+            else *reinterpret_cast<uint2*>(at + e * 16) = make_uint2(w[e][0], w[e][1]);
         }
     }
 }
@@ -397,12 +436,15 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append_i8_kernel(const _
         if (t < uint32_t(p.T)) rope_rows<HP>(p, int(t), int(r / cpr) * HP, p.Hq, int(r % cpr));
         return;
     }
-    __shared__ __align__(16) uint8_t stages[kRopeThreads / 32][16 * D * 2];
+    extern __shared__ __align__(16) uint8_t rope_smem[];
+    constexpr int kStage = 16 * D * 2, kWarps = kRopeThreads / 32;
+    float* table = reinterpret_cast<float*>(rope_smem);           // [16][rd]
+    uint8_t* stages = rope_smem + 16 * D * 4;                      // a tile a warp
     __shared__ int src[16];    // the call's token of each row of the block, -1: none
     __shared__ int not_first;  // another token of the block comes before
     // This CTA's tokens (at most 32); those right behind a token of their own
     // block cannot be its first.  Every warp sees the same mask.
-    const int lane = threadIdx.x & 31, t0 = blockIdx.x * p.tokens_per_cta;
+    const int lane = threadIdx.x & 31, t0 = int(blockIdx.x) / p.parts * p.tokens_per_cta;
     const bool here = lane < p.tokens_per_cta && t0 + lane < p.T;
     const int32_t my_slot = here ? __ldg(p.slot_mapping + t0 + lane) : -1;
     const int32_t before = here && t0 + lane > 0 ? __ldg(p.slot_mapping + t0 + lane - 1) : -1;
@@ -420,17 +462,41 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append_i8_kernel(const _
         if (threadIdx.x < 16) src[threadIdx.x] = -1;
         if (threadIdx.x == 0) not_first = 0;
         __syncthreads();
-#pragma unroll 8
-        for (int u = threadIdx.x; u < p.T; u += kRopeThreads) {
-            const int32_t s = __ldg(p.slot_mapping + u);
-            if (s < 0 || s / 16 != block) continue;
+        auto look = [&](int u, int32_t s) {
+            if (s < 0 || s / 16 != block) return;
             if (u < t) not_first = 1;
             atomicMax(&src[s & 15], u);  // of two tokens in one slot the later lands
+        };
+        const bool vec = (reinterpret_cast<uintptr_t>(p.slot_mapping) & 15) == 0;
+        const int whole = vec ? p.T / 4 : 0;
+#pragma unroll 8
+        for (int u = threadIdx.x; u < whole; u += kRopeThreads) {
+            const int4 s = __ldg(reinterpret_cast<const int4*>(p.slot_mapping) + u);
+            look(4 * u, s.x);
+            look(4 * u + 1, s.y);
+            look(4 * u + 2, s.z);
+            look(4 * u + 3, s.w);
         }
+        for (int u = 4 * whole + threadIdx.x; u < p.T; u += kRopeThreads) look(u, __ldg(p.slot_mapping + u));
         __syncthreads();
         if (not_first) continue;
-        for (int x = threadIdx.x >> 5; x < 2 * p.Hkv; x += kRopeThreads / 32)
-            quantize_tile<D>(p, src, block, x >> 1, x & 1, stages[threadIdx.x >> 5], lane);
+        // the angles of the block's rows, for every head; they land with the first tile
+        const int per_row = p.rd / 4;
+        for (int x = threadIdx.x; x < 16 * per_row; x += kRopeThreads) {
+            const int u = src[x / per_row];
+            if (u >= 0) cp_async16(table + x * 4, angles(p, u, false) + x % per_row * 4);
+        }
+        uint8_t* mine = stages + (threadIdx.x >> 5) * kStage;
+        const int step = p.parts * kWarps, tiles = 2 * p.Hkv;
+        for (int x = int(blockIdx.x) % p.parts * kWarps + (threadIdx.x >> 5), n = 0; n < tiles; x += step, n += step) {
+            __syncwarp();  // the tile before has been read
+            if (x < tiles) stage_rows<D>(p, src, x >> 1, x & 1, mine, lane);
+            cp_async_commit();
+            cp_async_wait_all();
+            if (n == 0) __syncthreads();  // the table
+            else __syncwarp();
+            if (x < tiles) quantize_tile<D>(p, src, block, x >> 1, x & 1, mine, table, lane);
+        }
     }
 }
 

@@ -309,10 +309,17 @@ pa_status launch_rope_i8(pa::RopeParams& p, cudaStream_t s) {
     // tokens few are their block's first, and a CTA looks at up to 16
     const int sms = sm_count();
     p.tokens_per_cta = p.T <= 4 * sms ? 1 : p.T / (4 * sms) < 16 ? p.T / (4 * sms) : 16;
-    p.kv_ctas = (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
+    // a tile per warp: as many CTAs as a block's tiles need, while there are SMs for them
+    const int groups = (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta, warps = pa::kRopeThreads / 32;
+    p.parts = (2 * p.Hkv + warps - 1) / warps;
+    while (p.parts > 1 && int64_t(groups) * p.parts > 12 * sms) --p.parts;
+    p.kv_ctas = groups * p.parts;
     const int64_t ctas = p.kv_ctas + (items + pa::kRopeThreads - 1) / pa::kRopeThreads;
     if (ctas > 0x7fffffff) return PA_ERR_SHAPE;
-    return launch_dependent(pa::rope_append_i8_kernel<D, HP>, dim3(unsigned(ctas)), pa::kRopeThreads, 0, s, p);
+    constexpr int smem = 16 * D * 4 + pa::kRopeThreads / 32 * 16 * D * 2;  // angles, a tile a warp
+    static unsigned attr_done[kMaxDevices];
+    if (!set_smem_once(pa::rope_append_i8_kernel<D, HP>, smem, attr_done)) return PA_ERR_CUDA;
+    return launch_dependent(pa::rope_append_i8_kernel<D, HP>, dim3(unsigned(ctas)), pa::kRopeThreads, smem, s, p);
 }
 
 pa_status append_i8(const Append& a, cudaStream_t s) {
