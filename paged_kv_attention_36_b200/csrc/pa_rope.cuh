@@ -7,8 +7,9 @@
 // (x_2i, x_2i+1) when interleaved, and becomes
 //     (a cos_i - b sin_i,  b cos_i + a sin_i)
 // with the angles' cosines and sines read from the caller's fp32 table
-// [max_position][rd] (rd/2 cosines, then rd/2 sines).  Products and sums are
-// single fp32 operations (no contraction), rounded once at the end.
+// [max_position][rd] (rd/2 cosines, then rd/2 sines), in fp32 and rounded once
+// at the end.  On the way to 8-bit codes each product and sum is rounded by
+// itself, so that the codes are those of the documented operations.
 #pragma once
 
 #include "pa_append.cuh"
@@ -71,8 +72,8 @@ __device__ __forceinline__ ChunkPair chunk_pair(int c, int rd, bool interleaved)
 }
 
 // Turns the 16 values of a chunk pair in place (8 angles, cosines cs[0..7], sines cs[rd/2 ..]).
-__device__ __forceinline__ void turn_chunks(uint4& lo, uint4& hi, const float (&c)[8], const float (&s)[8],
-                                            bool interleaved) {
+template <bool interleaved>
+__device__ __forceinline__ void turn_chunks(uint4& lo, uint4& hi, const float (&c)[8], const float (&s)[8]) {
     uint32_t* w[2] = {&lo.x, &hi.x};
     float x[16];
 #pragma unroll
@@ -83,12 +84,16 @@ __device__ __forceinline__ void turn_chunks(uint4& lo, uint4& hi, const float (&
             x[8 * h + 2 * j] = f.x;
             x[8 * h + 2 * j + 1] = f.y;
         }
-    if (interleaved) {
+    // two pairs at once; the rounding to bf16 leaves no room for the last bit of
+    // fp32, so products and sums are fused here
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) turn(x[i], x[8 + i], c[i], s[i]);
+    for (int i = 0; i < 8; i += 2) {
+        const int a0 = interleaved ? 2 * i : i, a1 = interleaved ? 2 * i + 2 : i + 1;
+        const int b0 = interleaved ? 2 * i + 1 : 8 + i, b1 = interleaved ? 2 * i + 3 : 9 + i;
+        const uint64_t a = f2_pack(x[a0], x[a1]), b = f2_pack(x[b0], x[b1]);
+        const uint64_t cc = f2_pack(c[i], c[i + 1]), ss = f2_pack(s[i], s[i + 1]), ns = f2_pack(-s[i], -s[i + 1]);
+        f2_unpack(f2_fma(a, cc, f2_mul(b, ns)), x[a0], x[a1]);
+        f2_unpack(f2_fma(b, cc, f2_mul(a, ss)), x[b0], x[b1]);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -142,7 +147,10 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, int t, int h0, in
         }
 #pragma unroll
         for (int i = 0; i < HP; ++i)
-            if (dst[i] && h0 + i < p.Hq + p.Hkv) turn_chunks(lo[i], hi[i], cs, sn, p.interleaved);
+            if (dst[i] && h0 + i < p.Hq + p.Hkv) {
+                if (p.interleaved) turn_chunks<true>(lo[i], hi[i], cs, sn);
+                else turn_chunks<false>(lo[i], hi[i], cs, sn);
+            }
     }
 #pragma unroll
     for (int i = 0; i < HP; ++i)
@@ -306,15 +314,25 @@ __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int* sr
         return NR == 16 ? all & 0xffffu : all >> (16 * half) & 0xffu;
     }();
     uint32_t top = 0;
+    if (v) {  // bf16 magnitudes as 16-bit integers, two at a time
+        uint32_t pair = 0;
+#pragma unroll 2
+        for (uint32_t left = have; left; left &= left - 1) {
+            const uint2 w = *reinterpret_cast<const uint2*>(stage + row_of(__ffs(left) - 1) * D * 2 + lo * 2);
+            pair = __vmaxu2(__vmaxu2(pair, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu);
+        }
+        top = max(pair << 16, pair & 0xffff0000u);
+    } else {
 #pragma unroll 1
-    for (uint32_t left = have; left; left &= left - 1) {
-        uint64_t x01, x23;
-        load(row_of(__ffs(left) - 1), x01, x23);
-        float x[4];
-        f2_unpack(x01, x[0], x[1]);
-        f2_unpack(x23, x[2], x[3]);
+        for (uint32_t left = have; left; left &= left - 1) {
+            uint64_t x01, x23;
+            load(row_of(__ffs(left) - 1), x01, x23);
+            float x[4];
+            f2_unpack(x01, x[0], x[1]);
+            f2_unpack(x23, x[2], x[3]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = max(top, abs_bits(x[e]));
+            for (int e = 0; e < 4; ++e) top = max(top, abs_bits(x[e]));
+        }
     }
     __syncwarp();
     top = __reduce_max_sync(0xffffffffu, top);
@@ -425,7 +443,7 @@ __device__ __forceinline__ void quantize_tile(const RopeParams& p, const int* sr
 }
 
 template <int D, int HP>
-__global__ void __launch_bounds__(kRopeThreads, 3) rope_append_i8_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_append_i8_kernel(const __grid_constant__ RopeParams p) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (int(blockIdx.x) >= p.kv_ctas) {  // the queries
@@ -463,7 +481,7 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append_i8_kernel(const _
         if (threadIdx.x == 0) not_first = 0;
         __syncthreads();
         auto look = [&](int u, int32_t s) {
-            if (s < 0 || s / 16 != block) return;
+            if (uint32_t(s) >> 4 != uint32_t(block)) return;  // padding is negative: in no block
             if (u < t) not_first = 1;
             atomicMax(&src[s & 15], u);  // of two tokens in one slot the later lands
         };
@@ -472,6 +490,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_append_i8_kernel(const _
 #pragma unroll 8
         for (int u = threadIdx.x; u < whole; u += kRopeThreads) {
             const int4 s = __ldg(reinterpret_cast<const int4*>(p.slot_mapping) + u);
+            if (uint32_t(s.x) >> 4 != uint32_t(block) && uint32_t(s.y) >> 4 != uint32_t(block) &&
+                uint32_t(s.z) >> 4 != uint32_t(block) && uint32_t(s.w) >> 4 != uint32_t(block))
+                continue;
             look(4 * u, s.x);
             look(4 * u + 1, s.y);
             look(4 * u + 2, s.z);

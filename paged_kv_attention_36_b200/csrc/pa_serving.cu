@@ -326,9 +326,9 @@ pa_status append_i8(const Append& a, cudaStream_t s) {
     pa::RopeParams p;
     const pa_status st = prepare_append(a, true, p);
     if (st != PA_OK || p.T == 0) return st;
-    const bool fours = rows_in_fours(int64_t(p.T) * p.Hq, p.D, sm_count());
-    if (p.D == 64) return fours ? launch_rope_i8<64, 4>(p, s) : launch_rope_i8<64, 1>(p, s);
-    return fours ? launch_rope_i8<128, 4>(p, s) : launch_rope_i8<128, 1>(p, s);
+    const bool many = rows_in_fours(int64_t(p.T) * p.Hq, p.D, sm_count());  // in twos here: four leave too few registers
+    if (p.D == 64) return many ? launch_rope_i8<64, 2>(p, s) : launch_rope_i8<64, 1>(p, s);
+    return many ? launch_rope_i8<128, 2>(p, s) : launch_rope_i8<128, 1>(p, s);
 }
 
 }  // namespace
