@@ -30,6 +30,7 @@
 
 #include "pa_decode.cuh"
 #include "pa_tcgen05.cuh"
+#include "pa_window.cuh"
 
 namespace pa {
 
@@ -64,44 +65,6 @@ __device__ __forceinline__ void imma_16832(int (&c)[4], const uint32_t (&a)[4], 
 // 12582912 + n while |n| < 2^22, so a subtraction converts it.
 constexpr int kIntBase = 0x4B400000;
 constexpr float kIntBaseF = 12582912.f;
-
-// Sliding window with sinks: of a context of L tokens the query sees tokens
-// 0 .. min(sinks, L)-1 and L-window .. L-1.  Only the pages that hold one of
-// them are listed, in order: `ns` pages of sinks before the window's first
-// page, then the window's pages; entry i is page i for i < ns and page
-// i + skip after that.  A page is listed once, whichever tokens of it are
-// seen (visible_tokens).
-struct WindowPages {
-    int32_t first;  // first token of the window
-    int32_t ns, skip, np;
-    __host__ __device__ __forceinline__ WindowPages(int32_t L, int32_t window, int32_t sinks) {
-        first = L > window ? L - window : 0;
-        const int32_t wpage = first / 16, spages = ((sinks < first ? sinks : first) + 15) / 16;
-        ns = spages < wpage ? spages : wpage;
-        skip = wpage - ns;
-        np = (L + 15) / 16 - skip;
-    }
-    __host__ __device__ __forceinline__ int32_t page(int32_t i) const { return i < ns ? i : i + skip; }
-};
-
-// Which of the 16 tokens of page pg a query at the end of L tokens sees.
-__host__ __device__ __forceinline__ uint32_t visible_tokens(int32_t pg, int32_t L, int32_t first, int32_t sinks) {
-    const int32_t t0 = pg * 16;
-    auto below = [](int32_t n) -> uint32_t {  // bits 0 .. n-1
-        return n <= 0 ? 0u : n >= 16 ? 0xffffu : (1u << n) - 1u;
-    };
-    return below(L - t0) & (~below(first - t0) | below(sinks < L ? sinks - t0 : 16));
-}
-
-// Page at which a share boundary at line position t cuts a segment of np
-// pages that starts at u0: 0 or np where fewer than `snap` pages (or half
-// the segment) would lie before or behind it.
-__host__ __device__ __forceinline__ int32_t cut_page(int64_t t, int64_t u0, int32_t np, int32_t snap) {
-    if (t <= u0) return 0;
-    if (t >= u0 + np) return np;
-    const int32_t c = int32_t(t - u0), lo = snap < (np + 1) / 2 ? snap : (np + 1) / 2;
-    return c < lo ? 0 : np - c < lo ? np : c;
-}
 
 // ---- page math over 8-bit codes ------------------------------------------------
 // Both products run on the integer tensor cores, so no code is ever
@@ -559,6 +522,11 @@ struct WideParams {
     int32_t window, sinks;
 };
 
+// The pages a decode over L > 0 tokens streams.
+__device__ __forceinline__ WindowPages window_pages(const WideParams& wp, int32_t L) {
+    return WindowPages(window_first(L - 1, wp.window), L, wp.sinks);
+}
+
 __device__ __forceinline__ void cp_async4(void* smem_dst, const void* gmem_src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)), "l"(gmem_src) : "memory");
 }
@@ -623,7 +591,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
     long long v_mine = 0, incl_mine = 0, Wt = 0;
     int32_t L_mine = 0;
     auto units = [&](int32_t L) -> long long {
-        return L > 0 ? (long long)(WindowPages(L, wp.window, wp.sinks).np + p.seg_weight) * p.NG : 0;
+        return L > 0 ? (long long)(window_pages(wp, L).np + p.seg_weight) * p.NG : 0;
     };
     for (int base = 0; base < p.B; base += NT) {
         const int b = base + threadIdx.x;
@@ -687,7 +655,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
             int32_t b, hg, L, j, npg;
             int64_t u0;  // line position of its first page
         };
-        auto pages_of = [&](const Seg& g) { return WindowPages(g.L, wp.window, wp.sinks); };
+        auto pages_of = [&](const Seg& g) { return window_pages(wp, g.L); };
         auto cut = [&](Seg& g, int32_t np) {
             g.j = cut_page(p_start, g.u0, np, sh.snap);
             g.npg = cut_page(p_end, g.u0, np, sh.snap) - g.j;
@@ -734,9 +702,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
                 if (ok) {
                     // the CTAs of the segment's first and last page
                     const int np = pages_of(seg).np;
-                    int k0 = split.owner(seg.u0), k1 = split.owner(seg.u0 + np - 1);
-                    if (cut_page(split.start(k0 + 1), seg.u0, np, sh.snap) == 0) ++k0;
-                    if (cut_page(split.start(k1), seg.u0, np, sh.snap) == np) --k1;
+                    int32_t k0, k1;
+                    segment_owners(split, seg.u0, np, sh.snap, k0, k1);
                     descs[s] = WideDesc{seg.b, seg.hg, seg.j, seg.npg, seg.L, k0, k1, 0};
                     mbar_arrive(&segfull[s]);
                 }
@@ -846,7 +813,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
         const int64_t row = int64_t(d.b) * p.Hq + int64_t(g) * G;  // its first query head
         st.load_q_global(p.q + row * (D * 2), lane, p.qscale);
         st.reset();
-        const WindowPages pages(d.L, wp.window, wp.sinks);
+        const WindowPages pages = window_pages(wp, d.L);
         // this part's pages: those whose running number is `part` modulo WPH
         auto advance = [&]() {
             slot += step;

@@ -164,21 +164,16 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
     const int first_pos = L - q_len;
     const int last_row = (row0 + Cfg::kBM < nrows ? row0 + Cfg::kBM : nrows) - 1;
     int nkeys = first_pos + last_row / G + 1;
-    int ns, skip;  // the list: ns pages of sinks, then the pages from the first row's window on
-    {
-        const int p0 = first_pos + row0 / G + 1;
-        const int f0 = p0 > p.window ? p0 - p.window : 0;
-        const int wpage = f0 / 16, spages = ((p.sinks < f0 ? p.sinks : f0) + 15) / 16;
-        ns = spages < wpage ? spages : wpage;
-        skip = wpage - ns;
-        nkeys -= skip * 16;
-    }
+    // the list: the pages of the sinks, then those from the first row's window on
+    const WindowPages listed(window_first(first_pos + row0 / G, p.window), nkeys, p.sinks);
+    const int skip = listed.skip;
+    nkeys -= skip * 16;
     const int32_t* bt = p.block_tables + int64_t(b) * p.M;
     const int pages = (nkeys + 15) / 16, nblk = (nkeys + BN - 1) / BN;
     // (block, kv head) tile of listed page pg; -1 past the list
     auto tile_of = [&](int pg) -> int {
         if (pg >= pages) return -1;
-        int32_t blk = __ldg(bt + (pg >= ns ? pg + skip : pg));
+        int32_t blk = __ldg(bt + listed.page(pg));
         if (blk < 0 || blk >= p.NB) {
             raise_error(PA_DEVERR_BLOCK_ID);
             blk = 0;
@@ -356,7 +351,7 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
         const bool valid = r < nrows;
         // list keys [0, sink) and [lo, lim) are visible (rows past the task as its last one)
         const int lim = valid ? first_pos + r / G + 1 - skip * 16 : nkeys;
-        const int lo = lim + skip * 16 > p.window ? lim - p.window : 0;
+        const int lo = window_first(lim - 1 + skip * 16, p.window) - skip * 16;
         const int sink = p.sinks < lim ? p.sinks : lim;
 
         // ---- Q row: a power of two times it, as f16, in shared memory ----

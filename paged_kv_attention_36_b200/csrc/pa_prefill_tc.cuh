@@ -51,6 +51,7 @@
 
 #include "pa_prefill.cuh"
 #include "pa_tcgen05.cuh"
+#include "pa_window.cuh"
 
 namespace pa {
 
@@ -139,11 +140,10 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         const int last_row = (row0 + Cfg::kBM < nrows ? row0 + Cfg::kBM : nrows) - 1;
         nkeys = first_pos + last_row / G + 1;  // tokens 0 .. nkeys-1 are visible to some row
         if constexpr (WINDOW) {
-            const int p0 = first_pos + row0 / G + 1;
-            f0 = p0 > p.window ? p0 - p.window : 0;
-            const int wpage = f0 / 16, spages = ((p.sinks < f0 ? p.sinks : f0) + 15) / 16;
-            ns = spages < wpage ? spages : wpage;
-            skip = wpage - ns;
+            f0 = window_first(first_pos + row0 / G, p.window);
+            const WindowPages w(f0, nkeys, p.sinks);
+            ns = w.ns;
+            skip = w.skip;
             f0 -= skip * 16;
             nkeys -= skip * 16;
         }
@@ -348,7 +348,8 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         const int lim = PREFIX ? nkeys : WINDOW ? (valid ? pos1 - skip * 16 : nkeys) : (valid ? pos1 : 1);
         int lo = 0, sink = 0;
         if constexpr (WINDOW) {
-            lo = lim + skip * 16 > p.window ? lim - p.window : 0;
+            const int from = window_first(lim - 1 + skip * 16, p.window);
+            lo = from - skip * 16;
             sink = p.sinks < lim ? p.sinks : lim;
         }
         const int64_t qrow = int64_t(PREFIX ? first : q0) + r / G;

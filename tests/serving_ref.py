@@ -91,8 +91,8 @@ def append_i8(k_rows, v_rows, slots, caches):
         by_block.setdefault(s // 16, {})[s % 16] = t
     for blk, rows in by_block.items():
         for g in range(k_cache.shape[1]):
-            for src, tile, scale in ((k_rows, k_cache[blk, g], k_scale),
-                                     (v_rows, v_cache[blk, g].t()[V_BYTES], v_scale)):
+            for is_v, src, tile, scale in ((False, k_rows, k_cache[blk, g], k_scale),
+                                           (True, v_rows, v_cache[blk, g].t()[V_BYTES], v_scale)):
                 offs = sorted(rows)
                 x = torch.stack([src[rows[o], g] for o in offs])
                 old = torch.tensor(0.0) if 0 in rows else scale[blk, g].clone()
@@ -106,10 +106,10 @@ def append_i8(k_rows, v_rows, slots, caches):
                 new = torch.round(x / now) if now > 0 else torch.zeros_like(x)
                 codes[offs] = new.to(torch.int8)
                 scale[blk, g] = now
-                if src is k_rows:
-                    k_cache[blk, g] = codes
-                else:
+                if is_v:
                     v_cache[blk, g][:, V_BYTES] = codes.t()
+                else:
+                    k_cache[blk, g] = codes
 
 
 def values_i8(k, v, ks, vs, blocks, L):
