@@ -16,7 +16,6 @@ FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden",
-    "--split-compile=0",
 ]
 
 # translation units, compiled side by side
