@@ -181,7 +181,7 @@ struct I8Math : MmaMath<D, G, 16> {
         float y[NP][4], lv[NP];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            lv[i] = fmaxf(__log2f(vs[i]), -100.f);  // a scale of 0: codes of 0, weight still in l
+            lv[i] = vs[i] <= 0x1p-100f ? -100.f : __log2f(vs[i]);  // a scale of 0: codes of 0, weight still in l
             const float c[2] = {qs[0] * ks[i], qs[1] * ks[i]};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

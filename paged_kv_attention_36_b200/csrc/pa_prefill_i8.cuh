@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
                 }
                 float x, y;
                 f2_unpack(f2_add(acc0, acc1), x, y);
-                l = fmaf(x + y, __shfl_sync(0xffffffffu, inv, pg), l);
+                const float by = __shfl_sync(0xffffffffu, inv, pg);
+                l = x + y != 0.f ? fmaf(x + y, by, l) : l;  // a page the row does not see: whatever its scale
             }
             tmem_st32(tmem + lanes + bb * BN, w);
             tmem_st_wait();

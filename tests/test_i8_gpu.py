@@ -228,3 +228,46 @@ def test_i8_device_errors(pa):
         assert pa.pa_device_errors(clear=True) == bits
         pa.pa_prefill_i8(q, cu, 1, k, v, ks, vs, table, cl, 0.1, out)
         assert pa.pa_device_errors(clear=True) == bits
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_nonfinite_scale_poisons_who_sees_it_only(pa, D, which):
+    # block 1 (tokens 16-31) of kv head 1 has a NaN scale: that head's queries
+    # that see it are NaN, its other queries and the other head are untouched
+    g = torch.Generator().manual_seed(D)
+    k, v, ks, vs, bt = ref.i8_batch(g, [100], 2, D)
+    clean = (ks.clone(), vs.clone())
+    (ks if which == "k" else vs)[bt[0, 1].long(), 1] = float("nan")
+    q = torch.randn((100, 8, D), generator=g).bfloat16()
+    cu = torch.tensor([0, 100], dtype=torch.int32).cuda()
+    cl = torch.tensor([100], dtype=torch.int32).cuda()
+    cache = [t.cuda() for t in (k, v, ks, vs, bt)]
+    want, mean_abs = ref.attend(q, *ref.values_i8(k, v, *clean, bt[0], 100), 0.1, 10, 3)
+    sees = torch.stack([ref.visible(100, p, 10, 3)[16:32].any() for p in range(100)])
+    out = torch.empty_like(q).cuda()
+    pa.pa_prefill_i8(q.cuda(), cu, 100, *cache, cl, 0.1, out, window=10, sinks=3)
+    got = out.cpu()
+    assert torch.isnan(got[sees][:, 4:]).all()
+    ref.assert_attention(got[:, :4], want[:, :4], mean_abs[:, :4], PREFILL_WEIGHTS)
+    ref.assert_attention(got[~sees][:, 4:], want[~sees][:, 4:], mean_abs[~sees][:, 4:], PREFILL_WEIGHTS)
+    for n, poisoned in ((30, True), (60, False)):
+        one = torch.empty_like(q[:1]).cuda()
+        pa.pa_decode_i8(q[n - 1:n].cuda(), *cache, torch.tensor([n], dtype=torch.int32).cuda(), 0.1, one, window=10,
+                        sinks=3)
+        ref.assert_attention(one[:, :4], want[n - 1:n, :4], mean_abs[n - 1:n, :4], DECODE_WEIGHTS)
+        if poisoned:
+            assert torch.isnan(one[:, 4:]).all()
+        else:
+            ref.assert_attention(one[:, 4:], want[n - 1:n, 4:], mean_abs[n - 1:n, 4:], DECODE_WEIGHTS)
+
+
+def test_decode_i8_zero_queries_and_scales(pa):
+    # all-zero queries, a scale of zero and a negative one
+    g = torch.Generator().manual_seed(31)
+    lens = [70, 5]
+    batch = ref.i8_batch(g, lens, 2, 64)
+    q = torch.randn((2, 8, 64), generator=g).bfloat16()
+    q[0, 3] = 0
+    for scale in (0.125, 0.0, -0.3):
+        _check_decode(pa, q, batch, lens, scale, ref.ALL, 0)
