@@ -648,9 +648,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
         const uint64_t pol = policy_evict_first();
         const uint32_t stage_tx = uint32_t(2 * HS * kTile);
 
-        // The segments of the share in order; block ids are read one batch
-        // of stages ahead, over segment ends too, so that no page waits for
-        // the block table.
+        // The segments of the share in order; within a segment block ids are
+        // read one batch of stages ahead.
         struct Seg {
             int32_t b, hg, L, j, npg;
             int64_t u0;  // line position of its first page
@@ -714,13 +713,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
             const int nst = seg.npg << sh.SPL_LOG;
             Seg next = seg;
             for (int c0 = 0; ok && c0 < nst; c0 += C) {
-                int32_t blk_next;
-                if (c0 + C < nst) {
-                    blk_next = block_of(seg, c0 + C);
-                } else {
-                    next = after(seg, L_next);
-                    blk_next = next.u0 < p_end ? block_of(next, 0) : 0;
-                }
+                int32_t blk_next = c0 + C < nst ? block_of(seg, c0 + C) : 0;
                 const int n = (nst - c0) < C ? (nst - c0) : C;
                 bool lane_ok = true;
                 if (lane < n) {
@@ -758,6 +751,12 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
                     }
                 }
                 ok = __all_sync(0xffffffffu, lane_ok);
+                if (c0 + C >= nst) {
+                    // the next segment's first ids, once this one's last copies
+                    // are under way (a call of few pages starts them that much sooner)
+                    next = after(seg, L_next);
+                    if (next.u0 < p_end) blk_next = block_of(next, 0);
+                }
                 blk = blk_next;
                 slot0 += n;
                 if (slot0 >= R) {
