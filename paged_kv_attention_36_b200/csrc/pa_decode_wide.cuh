@@ -127,6 +127,12 @@ struct I8Math : MmaMath<D, G, 16> {
             }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // v * down is exact and at most 4, so the product with r neither
+        // overflows nor vanishes, however large or small q is
+        int e = int(__float_as_uint(top) >> 23) - 127;
+        e = e < -126 ? -126 : e > 126 ? 126 : e;
+        const float down = __uint_as_float(uint32_t(127 - e) << 23);
+        const float r = top > 0.f ? 32512.f / (top * down) : 0.f;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
 #pragma unroll
@@ -136,8 +142,7 @@ struct I8Math : MmaMath<D, G, 16> {
                 uint32_t hi = 0, lo = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    // v / top first: the quotient is at most 1 however large or small q is
-                    const int q16 = top > 0.f ? __float2int_rn(v[e] / top * 32512.f) : 0;
+                    const int q16 = __float2int_rn(v[e] * down * r);
                     const int up = (q16 + 128) >> 8;
                     hi |= uint32_t(up & 0xff) << (8 * e);
                     lo |= uint32_t((q16 - (up << 8)) & 0xff) << (8 * e);
@@ -613,7 +618,8 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
     const int64_t want = (Wt + p.min_pages - 1) / p.min_pages;
     const int64_t grid_eff = want < int64_t(gridDim.x) ? want : int64_t(gridDim.x);
     if (Wt == 0 || int64_t(blockIdx.x) >= grid_eff) return;
-    const Split split{Wt / grid_eff, Wt % grid_eff};
+    const Split split = Wt >> 31 ? Split{Wt / grid_eff, Wt % grid_eff}
+                                 : Split{int32_t(Wt) / int32_t(grid_eff), int32_t(Wt) % int32_t(grid_eff)};
     const int64_t p_start = split.start(blockIdx.x), p_end = split.start(int64_t(blockIdx.x) + 1);
     auto locate = [&](int b, long long v, long long incl, int32_t L) {
         if (v > 0 && incl - v <= p_start && p_start < incl) {
@@ -660,7 +666,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
             g.npg = cut_page(p_end, g.u0, np, sh.snap) - g.j;
         };
         // The segment after g (u0 >= p_end: none); L_next: the length of
-        // sequence g.b + 1, read ahead.
+        // sequence g.b + 1, read ahead and not checked.
+        auto checked = [&](int32_t L) {
+            const int64_t cap = int64_t(p.M) * 16;
+            return L < 0 ? 0 : L > cap ? int32_t(cap) : L;
+        };
         auto after = [&](const Seg& g, int32_t L_next) {
             Seg n = g;
             do {
@@ -669,9 +679,9 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
                 if (++n.hg == p.NG) {
                     n.hg = 0;
                     ++n.b;
-                    n.L = L_next;
+                    n.L = checked(L_next);
                     while (n.L == 0) n.L = clamp_len<16>(p, ++n.b, false);
-                    if (n.b + 1 < p.B) L_next = clamp_len<16>(p, n.b + 1, false);
+                    if (n.b + 1 < p.B) L_next = __ldg(p.context_lens + n.b + 1);
                 }
                 cut(n, pages_of(n).np);
             } while (n.npg == 0);
@@ -688,21 +698,22 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
         seg.b = misc->b0;
         seg.L = misc->L0;
         const int64_t unit0 = pages_of(seg).np + p.seg_weight;
-        seg.hg = int((p_start - misc->pre0) / unit0);
+        seg.hg = p_start - misc->pre0 < unit0 ? 0 : int((p_start - misc->pre0) / unit0);
         seg.u0 = misc->pre0 + int64_t(seg.hg) * unit0;
         cut(seg, pages_of(seg).np);
-        if (seg.npg == 0) seg = after(seg, seg.b + 1 < p.B ? clamp_len<16>(p, seg.b + 1, false) : 0);
+        if (seg.npg == 0) seg = after(seg, seg.b + 1 < p.B ? __ldg(p.context_lens + seg.b + 1) : 0);
         int32_t blk = seg.u0 < p_end ? block_of(seg, 0) : 0;
         while (ok && seg.u0 < p_end) {
-            const int32_t L_next = seg.b + 1 < p.B ? clamp_len<16>(p, seg.b + 1, false) : 0;
+            // (as it is: checked where it is used, so that nothing waits for it here)
+            const int32_t L_next = seg.b + 1 < p.B ? __ldg(p.context_lens + seg.b + 1) : 0;
             if (lane == 0) {
                 const int s = seg_i % S;
                 if (seg_i >= S) ok = mbar_wait(&segempty[s], ((seg_i / S) - 1) & 1, abort);
                 if (ok) {
                     // the CTAs of the segment's first and last page
                     const int np = pages_of(seg).np;
-                    int32_t k0, k1;
-                    segment_owners(split, seg.u0, np, sh.snap, k0, k1);
+                    int32_t k0 = int(blockIdx.x), k1 = k0;
+                    if (seg.npg < np) segment_owners(split, seg.u0, np, sh.snap, k0, k1);
                     descs[s] = WideDesc{seg.b, seg.hg, seg.j, seg.npg, seg.L, k0, k1, 0};
                     mbar_arrive(&segfull[s]);
                 }
