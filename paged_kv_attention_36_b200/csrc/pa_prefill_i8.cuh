@@ -170,10 +170,10 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
     nkeys -= skip * 16;
     const int32_t* bt = p.block_tables + int64_t(b) * p.M;
     const int pages = (nkeys + 15) / 16, nblk = (nkeys + BN - 1) / BN;
-    // (block, kv head) tile of listed page pg; -1 past the list
+    // (block, kv head) tile of listed page pg; past the list its last page again
+    // (masked, and not multiplied)
     auto tile_of = [&](int pg) -> int {
-        if (pg >= pages) return -1;
-        int32_t blk = __ldg(bt + listed.page(pg));
+        int32_t blk = __ldg(bt + listed.page(pg < pages ? pg : pages - 1));
         if (blk < 0 || blk >= p.NB) {
             raise_error(PA_DEVERR_BLOCK_ID);
             blk = 0;
@@ -274,8 +274,7 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
         auto fetch = [&](const int8_t* cache, const int (&t)[NP], uint4 (&r)[NP]) {
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                r[i] = t[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(cache + int64_t(t[i]) * (16 * D) + off))
-                                 : make_uint4(0u, 0u, 0u, 0u);
+                r[i] = __ldg(reinterpret_cast<const uint4*>(cache + int64_t(t[i]) * (16 * D) + off));
         };
         tiles_of(0, tl);
         fetch(pp.k_cache, tl, kr);
@@ -296,17 +295,16 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
                 uint8_t* kb = stages + s * Cfg::kStage;
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
+                    // two 16-byte chunks of the row; the second panel's threads write
+                    // theirs in the other order, into the banks the first's leave
+                    const bool f = D == 128 && cc >= 4;
                     uint32_t o[8];
-                    codes_to_f16<false>(kr[i], o);
-                    const int row = page_in_block(i) * 16 + t_in;
+                    codes_to_f16<false>(f ? make_uint4(kr[i].z, kr[i].w, kr[i].x, kr[i].y) : kr[i], o);
+                    const int row = page_in_block(i) * 16 + t_in;  // row % 8 = t_in % 8
                     uint8_t* dst = kb + (cc >> 2) * Cfg::kPanelK + row * 128;
-                    const int ch = (cc & 3) * 2;  // 16-byte chunk of the row, two of them; the second
-                                                  // panel's threads write theirs in the other order
-                    const int f = (cc >> 2) & 1;
-                    *reinterpret_cast<uint4*>(dst + (((ch + f) ^ (row & 7)) << 4)) =
-                        f ? make_uint4(o[4], o[5], o[6], o[7]) : make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4*>(dst + (((ch + 1 - f) ^ (row & 7)) << 4)) =
-                        f ? make_uint4(o[0], o[1], o[2], o[3]) : make_uint4(o[4], o[5], o[6], o[7]);
+                    const int ch = ((cc & 3) * 2) ^ (t_in & 7) ^ (f ? 1 : 0);
+                    *reinterpret_cast<uint4*>(dst + (ch << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst + ((ch ^ 1) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&k_full[s]);
@@ -393,11 +391,10 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
         }
         const bool positive = ce > 0.f;
 
-        // lane i < 4 of each warp holds page i's scales, read one block ahead
-        auto scale_at = [&](const float* scales, int t) { return t >= 0 ? __ldg(scales + t) : 0.f; };
-        auto page_tile = [&](int j) { return lane < Cfg::kPages ? tile_of(j * Cfg::kPages + lane) : -1; };
-        int tl = page_tile(0);
-        float ks_next = scale_at(pp.k_scale, tl), vs_next = scale_at(pp.v_scale, tl);
+        // lane i of each warp holds page i % 4's scales, read one block ahead
+        auto page_tile = [&](int j) { return tile_of(j * Cfg::kPages + (lane & (Cfg::kPages - 1))); };
+        const int tl = page_tile(0);
+        float ks_next = __ldg(pp.k_scale + tl), vs_next = __ldg(pp.v_scale + tl);
         int tl_next = page_tile(1);
 
         float m = -INFINITY, l = 0.f;
@@ -405,8 +402,8 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
         for (int j = 0; j < nblk; ++j) {
             const int bb = j % NS, n0 = j * BN;
             const float ks = ks_next, vs = vs_next;
-            ks_next = scale_at(pp.k_scale, tl_next);
-            vs_next = scale_at(pp.v_scale, tl_next);
+            ks_next = __ldg(pp.k_scale + tl_next);
+            vs_next = __ldg(pp.v_scale + tl_next);
             tl_next = page_tile(j + 2);
             // a scale of 0 (its codes are 0 too) as one that changes nothing; NaN stays
             const float lvl = vs <= 0x1p-100f ? -100.f : __log2f(vs);
