@@ -140,12 +140,10 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
     int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
     volatile int* abort = s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = blockIdx.y;
 
     // ---- this tile's rows and the pages it attends ----
-    const int b = int(blockIdx.x) / p.tiles_per_seq;
-    const int tile = int(blockIdx.x) - b * p.tiles_per_seq;
-    if (b >= p.B) return;
+    const TileOfCta cta(p);
+    const int b = cta.b, tile = cta.tile, g = cta.g;
     const bool report = tile == 0 && g == 0 && threadIdx.x == 0;
     int L = __ldg(p.context_lens + b);
     const int64_t cap = int64_t(p.M) * 16;

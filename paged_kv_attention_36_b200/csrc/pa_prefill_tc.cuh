@@ -55,6 +55,30 @@
 
 namespace pa {
 
+// Which (sequence, 128-row tile, kv head) a CTA of the windowed and 8-bit calls
+// takes: sequences from the longest context to the shortest (in their order
+// beyond 32), a sequence's tiles from the last to the first, its kv heads side
+// by side, so that the long tiles do not start last (8-bit chunks: the last
+// wave took 9 % of the time) and a sequence's pages are read close together.
+struct TileOfCta {
+    int b, tile, g;
+    __device__ __forceinline__ TileOfCta(const PrefillParams& p) {
+        const int r = int(blockIdx.x) / p.Hkv, lane = threadIdx.x & 31;
+        g = int(blockIdx.x) - r * p.Hkv;
+        b = r / p.tiles_per_seq;
+        tile = p.tiles_per_seq - 1 - (r - b * p.tiles_per_seq);
+        if (p.B <= 32) {
+            const int32_t mine = lane < p.B ? __ldg(p.context_lens + lane) : -1;
+            int longer = 0;  // sequences before this lane's
+            for (int i = 0; i < p.B; ++i) {
+                const int32_t other = __shfl_sync(0xffffffffu, mine, i);
+                longer += other > mine || (other == mine && i < lane);
+            }
+            b = __ffs(__ballot_sync(0xffffffffu, lane < p.B && longer == b)) - 1;
+        }
+    }
+};
+
 template <int D, int BN, int KS, int NS>
 struct TcPrefillCfg {
     static constexpr int kBM = 128;                 // query rows of a CTA
@@ -109,7 +133,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     __shared__ int s_abort;
     volatile int* abort = &s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = blockIdx.y;
+    int g = blockIdx.y;
 
     // ---- this tile's rows and the key pages it attends ----
     int nrows, row0, nkeys;  // rows of the task, the tile's first row, keys staged (0 .. nkeys-1)
@@ -117,8 +141,14 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     int L = 0, q0 = 0, first_pos = 0, first = 0, P = 0, pg0 = 0;
     int ns = 0, skip = 0, f0 = 0;  // WINDOW: f0 = list key of the first row's first window token
     if constexpr (!PREFIX) {
-        const int b = int(blockIdx.x) / p.tiles_per_seq;
-        const int tile = int(blockIdx.x) - b * p.tiles_per_seq;
+        int b = int(blockIdx.x) / p.tiles_per_seq;
+        int tile = int(blockIdx.x) - b * p.tiles_per_seq;
+        if constexpr (WINDOW) {
+            const TileOfCta mine(p);
+            b = mine.b;
+            tile = mine.tile;
+            g = mine.g;
+        }
         if (b >= p.B) return;
         const bool report = tile == 0 && g == 0 && threadIdx.x == 0;
         L = __ldg(p.context_lens + b);

@@ -54,7 +54,7 @@ pa_status check_prefill(const Call& c, bool* done) {
         return PA_ERR_ALIGN;
     if (int64_t(d.num_blocks) * d.num_kv_heads * d.block_size >= (int64_t(1) << 31)) return PA_ERR_SHAPE;
     const int64_t tiles = (int64_t(c.max_q_len) * G + 127) / 128;
-    if (int64_t(d.num_seqs) * tiles > 0x7fffffffLL || d.num_kv_heads > 65535) return PA_ERR_SHAPE;
+    if (tiles > 0x7fffffffLL || int64_t(d.num_seqs) * tiles > 0x7fffffffLL / d.num_kv_heads) return PA_ERR_SHAPE;
     *done = false;
     return PA_OK;
 }
@@ -367,7 +367,7 @@ pa_status pa_prefill_window(const void* q, const int32_t* cu_q_lens, int32_t max
         !make_panel_map(&p.tmap_v, v_cache, cache_tiles, d.head_dim, d.block_size))
         return PA_ERR_CUDA;
     fill_prefill(c, p);
-    const dim3 grid(unsigned(d.num_seqs * p.tiles_per_seq), unsigned(d.num_kv_heads));
+    const dim3 grid(unsigned(d.num_seqs * p.tiles_per_seq * d.num_kv_heads));
     return by_shape(d, PrefillWindow{p, grid, static_cast<cudaStream_t>(stream)});
 }
 
@@ -387,7 +387,7 @@ pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_l
     p.v_cache = static_cast<const int8_t*>(v_cache);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    const dim3 grid(unsigned(dims->num_seqs * p.a.tiles_per_seq), unsigned(dims->num_kv_heads));
+    const dim3 grid(unsigned(dims->num_seqs * p.a.tiles_per_seq * dims->num_kv_heads));
     return by_shape(*dims, PrefillI8{p, grid, static_cast<cudaStream_t>(stream)});
 }
 

@@ -291,3 +291,32 @@ def test_wrong_device_and_shapes_are_refused(pa):
         pa.pa_rope_append(q, rows, rows, cl, torch.zeros((4, 40), device="cuda"), cl, out, kc, kc)
     assert e.value.code == -3
     assert pa.pa_device_errors(clear=True) == 0
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("B", [32, 33, 70])
+def test_multi_query_many_sequences(pa, i8, B):
+    # up to 32 sequences are taken from the longest on, more in their order; some bring nothing
+    g = torch.Generator().manual_seed(B)
+    Hq, Hkv, D = 4, 2, 64
+    lens = torch.randint(0, 200, (B,), generator=g).tolist()
+    chunks = [min(n, int(c)) for n, c in zip(lens, torch.randint(0, 60, (B,), generator=g))]
+    lens[5] = lens[6] = lens[7] = 64  # equal lengths
+    chunks[5], chunks[6], chunks[7] = 64, 0, 1
+    if i8:
+        k, v, ks, vs, bt = ref.i8_batch(g, lens, Hkv, D)
+        cache, seqs = (k, v, ks, vs), [ref.values_i8(k, v, ks, vs, bt[b], n) for b, n in enumerate(lens)]
+    else:
+        keys, values, kp, vp, bt = ref.bf16_batch(g, lens, Hkv, D)
+        cache, seqs = (kp, vp), [(a.double(), b.double()) for a, b in zip(keys, values)]
+    q = torch.randn((sum(chunks), Hq, D), generator=g).bfloat16()
+    cu = [0] + torch.tensor(chunks).cumsum(0).tolist()
+    out = torch.full_like(q, float("nan")).cuda()
+    call = pa.pa_prefill_i8 if i8 else pa.pa_prefill_window
+    call(q.cuda(), torch.tensor(cu, dtype=torch.int32).cuda(), max(chunks), *[t.cuda() for t in cache], bt.cuda(),
+         torch.tensor(lens, dtype=torch.int32).cuda(), 0.125, out, window=77, sinks=9)
+    assert pa.pa_device_errors(clear=True) == 0
+    for b in range(B):
+        rows = slice(cu[b], cu[b + 1])
+        want, mean_abs = ref.attend(q[rows], *seqs[b], 0.125, 77, 9)
+        ref.assert_attention(out[rows], want, mean_abs, 2.0 ** -8)
