@@ -1,29 +1,42 @@
 // pa_decode_wide.cuh -- paged decode with a sliding window, and over 8-bit
 // caches with a scale for each (block, kv head).
 //
-// The work line, the ring of TMA-staged pages, the split-KV partials and
-// their merge are those of pa_decode.cuh.  What differs:
+// The work line, the ring of TMA-staged pages and the split-KV pieces are those
+// of pa_decode.cuh.  What differs:
 //
-//   * Several warps share a kv head.  A CTA has 16 consumer warps, WPH = the
-//     largest power of two <= 16 / HG of them per head of the head group;
-//     part w of a head takes the pages whose running number is w modulo WPH
-//     and keeps a softmax state of its own.  At a segment's end the parts
-//     meet in shared memory and part 0 finishes the segment while the others
-//     go on.  The page math is a dependent chain (ldmatrix, convert, mma,
-//     max, exp2, mma), so one warp per head leaves the SM's issue slots
-//     empty: at half the bytes per token that chain, not HBM, was the bound
-//     of the fp8 decode (one warp per head: 34 % issue, 55 % DRAM).
+//   * A CTA has 8 consumer warps, WPH = the largest power of two <= 8 / HG of
+//     them per head of the head group; part w of a head takes the pages whose
+//     running number is w modulo WPH and keeps a softmax state of its own.  At
+//     a segment's end the parts meet in shared memory and part 0 finishes the
+//     segment while the others go on.  (Sixteen warps hold twice the stages, of
+//     which fewer are then in flight: 72 against 62 us on the 8-bit batch, 92
+//     against 73 us on one long context.)
+//   * A head group's page (at most 8 KB of K) is one ring stage; wider groups
+//     are cut into groups, which also halves the bytes of a piece where long
+//     contexts are merged.
 //   * Only the pages that a window or a sink reaches are on the line
 //     (WindowPages), and each page comes with a 16-bit mask of the tokens
 //     that count.
 //   * Share boundaries that would cut fewer than `snap` pages off a segment
 //     move to the segment's end (cut_page): short contexts stay whole, so a
 //     small batch needs no merge between CTAs.
+//   * Pieces are stored as the accumulator fragments lie (RawPiece), 16 bytes
+//     at a time; two pieces are folded in registers by whichever CTA is last,
+//     more are merged in one level or, past kWideFanIn, in two of about
+//     sqrt(pieces).
 //   * A page of an 8-bit cache brings its heads' scales along: two bulk
 //     copies where they are 16-byte pieces (kv heads in fours), else 4-byte
 //     cp.async copies that arrive on the stage's barrier.
 //   * Launched as a programmatic dependent: the set-up overlaps the end of
 //     the kernel before it.
+//
+// Bound by HBM.  Measured on B200 (floor: bytes at 6548 GB/s): 8-bit, batch 128
+// of 512-4096 tokens, 32/8 heads of 64: 57.1 us (floor 48.8); 8-bit, one
+// context of 131072 among 63 of 1024, 32/8 heads of 128: 68.8 us (61.5);
+// window 1024 and 4 sinks over the first batch in bf16: 47.2 us (40.6).  What is
+// left is the launch and the share scan (2 us), CTAs that stream slower than
+// the median (3 us) and the last merge (1-4 us); four short sequences take
+// 5.4-6.3 us, a chain of dependent loads.
 #pragma once
 
 #include <type_traits>
@@ -69,10 +82,10 @@ constexpr float kIntBaseF = 12582912.f;
 // ---- page math over 8-bit codes ------------------------------------------------
 // Both products run on the integer tensor cores, so no code is ever
 // converted: the tiles (K [16][D], V transposed in its token order) are A
-// operands of mma.sync m16n8k32 as ldmatrix delivers them.  (Converting them
-// to f16 took 24 of the 48 ALU instructions of a 64-wide page and twice the
-// mma; m16n8k32 s8 issues at the rate of m16n8k16 f16 here.)  The other
-// operand is fixed point in 16 bits, as two 8-bit halves:
+// operands of mma.sync m16n8k32 as ldmatrix delivers them.  (Converted to f16
+// by byte permutes, the same batch took 65-67 us and was bound by the ALU
+// chain; an s8 m16n8k32 takes 2.0 cycles of an SM, as an f16 m16n8k16 does.)
+// The other operand is fixed point in 16 bits, as two 8-bit halves:
 //
 //   q = qmax / 32512 * (256 hi + lo), hi and lo signed: off by at most 2^-16
 //     of the row's largest value.  S = 256 (K hi) + K lo, exact in integers.

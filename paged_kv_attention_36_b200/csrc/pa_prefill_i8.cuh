@@ -25,8 +25,11 @@
 //     is 2^-31 of the heaviest contribution.
 //   * setmaxnreg moves registers from the converters to the softmax.
 //
-// What bounds it: the softmax warps, as in the bf16 kernel; the converters
-// (about 1.1 instructions a code) fill issue slots that those leave.
+// Bound by the softmax's dependent chain, as the bf16 kernel is, and by the
+// issue slots that the converters share with it (51 % issued, tensor pipe
+// 26 %; with the converters' work taken out the same calls took 401 us).
+// Measured on B200: 16 chunks of 512 tokens behind 0-3500, 32/8 heads of 128:
+// 475 us, 566 TFLOP/s of visible pairs (floor at 1624 TFLOP/s: 166 us).
 #pragma once
 
 #include "pa_prefill_tc.cuh"

@@ -113,8 +113,11 @@ pa_status launch_dependent(Kernel kern, dim3 grid, int threads, int smem, cudaSt
 }
 
 // ---- wide decode ---------------------------------------------------------------
-constexpr int kWideStageK = 8192;      // K bytes of a ring stage, at most
-constexpr int kWideMinBytes = 65536;   // K+V bytes worth a CTA of their own
+constexpr int kWideStageK = 8192;      // K bytes of a ring stage, at most (windowed batch: 48.0 us, 49.5 us at 16 KB)
+// K+V bytes worth a CTA of their own (4 short sequences: 5.4 us; 8.1 us at
+// 4 KB, where contexts are cut and merged, 7.3 us at 256 KB, where CTAs queue
+// them; a batch of 128 does not notice)
+constexpr int kWideMinBytes = 65536;
 constexpr int kMaxSmem = 232448;
 
 int floor_log2(int x) {
@@ -290,7 +293,8 @@ pa_status prepare_append(const Append& a, bool i8, pa::RopeParams& p) {
 }
 
 // Rows a thread takes: four share one read of the angles once there are enough
-// threads for every SM without (2048 each).
+// threads for every SM without (2048 each): 8192 tokens 37.8 us against 41.6 us
+// a row each; a step of 128 tokens 3.7 us a row each, 3.9 us in fours.
 bool rows_in_fours(int64_t rows, int D, int sms) { return rows * (D / 16) >= int64_t(4) * 2048 * sms; }
 
 template <int HP>
@@ -305,11 +309,13 @@ template <int D, int HP>
 pa_status launch_rope_i8(pa::RopeParams& p, cudaStream_t s) {
     const int64_t items = int64_t(p.T) * ((p.Hq + HP - 1) / HP) * (D / 16);
     if (items >= int64_t(1) << 32) return PA_ERR_SHAPE;
-    // a decode step's tokens have a block each and a CTA each; of a long call's
-    // tokens few are their block's first, and a CTA looks at up to 16
+    // a decode step's tokens have a block each and a CTA each (128 tokens: 4.9 us,
+    // 31.9 us with 16 to a CTA); of a long call's tokens few are their block's
+    // first, and a CTA looks at up to 16 (7295 tokens: 56.7 us, 59.4 us with one)
     const int sms = sm_count();
     p.tokens_per_cta = p.T <= 4 * sms ? 1 : p.T / (4 * sms) < 16 ? p.T / (4 * sms) : 16;
-    // a tile per warp: as many CTAs as a block's tiles need, while there are SMs for them
+    // a tile per warp: as many CTAs as a block's tiles need, while there are SMs
+    // for them (128 tokens, 8 kv heads: 4.9 us, 6.6 us with two tiles a warp)
     const int groups = (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta, warps = pa::kRopeThreads / 32;
     p.parts = (2 * p.Hkv + warps - 1) / warps;
     while (p.parts > 1 && int64_t(groups) * p.parts > 12 * sms) --p.parts;
