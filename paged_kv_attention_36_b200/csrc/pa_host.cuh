@@ -145,12 +145,15 @@ bool dims_ok(const pa_dims* d) {
 }
 
 template <typename Kernel>
-bool set_smem_once(Kernel kern, int bytes, unsigned* done_mask_per_device) {
+bool set_smem_once(Kernel kern, int bytes, unsigned* done_mask_per_device, bool wide_clusters = false) {
     const int dev = current_device();
     if (dev < 0 || dev >= kMaxDevices) return false;
     std::lock_guard<std::mutex> lock(g_mu);
     if (!done_mask_per_device[dev]) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+            return false;
+        // clusters of more than 8 CTAs
+        if (wide_clusters && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
             return false;
         done_mask_per_device[dev] = 1;
     }

@@ -24,12 +24,13 @@
 //     when one passes it by 15: P lies in [0, 2^15], and f16's smallest step
 //     is 2^-31 of the heaviest contribution.
 //   * setmaxnreg moves registers from the converters to the softmax.
+//   * SPLIT: a cluster of CTAs shares each tile's keys (KeySplit).
 //
 // Bound by the softmax's dependent chain, as the bf16 kernel is, and by the
 // issue slots that the converters share with it (51 % issued, tensor pipe
 // 26 %; with the converters' work taken out the same calls took 401 us).
 // Measured on B200: 16 chunks of 512 tokens behind 0-3500, 32/8 heads of 128:
-// 475 us, 566 TFLOP/s of visible pairs (floor at 1624 TFLOP/s: 166 us).
+// 472 us, 570 TFLOP/s of visible pairs (floor at 1624 TFLOP/s: 166 us).
 #pragma once
 
 #include "pa_prefill_tc.cuh"
@@ -120,7 +121,7 @@ __device__ __forceinline__ void codes_to_f16(const uint4& r, uint32_t (&o)[8]) {
     }
 }
 
-template <int D, int G>
+template <int D, int G, bool SPLIT>
 __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kernel(const __grid_constant__
                                                                                   PrefillI8Params pp) {
     using Cfg = I8PrefillCfg<D>;
@@ -142,10 +143,14 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     int* s_abort = reinterpret_cast<int*>(tmem_slot + 1);
     volatile int* abort = s_abort;
+    int& s_ranks = s_abort[1];  // CTAs that share the tile
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
     // ---- this tile's rows and the pages it attends ----
-    const TileOfCta cta(p);
+    const TileOfCta cta(p, int(SPLIT ? blockIdx.x / cluster_size() : blockIdx.x));
     const int b = cta.b, tile = cta.tile, g = cta.g;
     const bool report = tile == 0 && g == 0 && threadIdx.x == 0;
     int L = __ldg(p.context_lens + b);
@@ -169,12 +174,29 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
     const WindowPages listed(window_first(first_pos + row0 / G, p.window), nkeys, p.sinks);
     const int skip = listed.skip;
     nkeys -= skip * 16;
+    int pages = (nkeys + 15) / 16, nblk = (nkeys + BN - 1) / BN;
     const int32_t* bt = p.block_tables + int64_t(b) * p.M;
-    const int pages = (nkeys + 15) / 16, nblk = (nkeys + BN - 1) / BN;
+    int ns = listed.ns, shift = skip * 16, sinks = p.sinks;
+    if constexpr (SPLIT) {
+        const KeySplit split(nblk);
+        if (int(cluster_rank()) >= split.ranks) return;  // before any barrier or TMEM use
+        if (threadIdx.x == 0) s_ranks = split.ranks;
+        // the list from this rank's first block on: pages, keys and sinks count from there
+        const int first_pg = int(cluster_rank()) * split.per * Cfg::kPages;
+        bt += first_pg;
+        ns -= first_pg;
+        shift += first_pg * 16;
+        sinks -= first_pg * 16;
+        nkeys -= first_pg * 16;
+        pages -= first_pg;
+        if (pages > split.per * Cfg::kPages) pages = split.per * Cfg::kPages;
+        nblk = (pages + Cfg::kPages - 1) / Cfg::kPages;
+    }
     // (block, kv head) tile of listed page pg; past the list its last page again
     // (masked, and not multiplied)
     auto tile_of = [&](int pg) -> int {
-        int32_t blk = __ldg(bt + listed.page(pg < pages ? pg : pages - 1));
+        if (pg >= pages) pg = pages - 1;
+        int32_t blk = __ldg(bt + (pg < ns ? pg : pg + skip));
         if (blk < 0 || blk >= p.NB) {
             raise_error(PA_DEVERR_BLOCK_ID);
             blk = 0;
@@ -349,9 +371,9 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
         const int r = row0 + row;
         const bool valid = r < nrows;
         // list keys [0, sink) and [lo, lim) are visible (rows past the task as its last one)
-        const int lim = valid ? first_pos + r / G + 1 - skip * 16 : nkeys;
-        const int lo = window_first(lim - 1 + skip * 16, p.window) - skip * 16;
-        const int sink = p.sinks < lim ? p.sinks : lim;
+        const int lim = valid ? first_pos + r / G + 1 - shift : nkeys;
+        const int lo = window_first(lim - 1 + shift, p.window) - shift;
+        const int sink = sinks < lim ? sinks : lim;
 
         // ---- Q row: a power of two times it, as f16, in shared memory ----
         float ce, bias;  // logits = (s - bias) * ce * k_scale
@@ -510,7 +532,19 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
                             mbar_wait_sleep(&v_empty[(nblk - 1) % KS], uint32_t((nblk - 1) / KS) & 1, abort));
         constexpr int kRowStride = D * 2 + 16;
         static_assert(Cfg::kBM * kRowStride <= Cfg::kBarOff, "output staging");
-        if (ok) {
+        if (SPLIT && s_ranks > 1) {
+            if (ok) {  // this rank's sums, for the cluster
+                static_assert(SplitRows<D>::kBytes <= Cfg::kBarOff, "split staging");
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[32];
+                    tmem_ld32(t_o + lanes + 32 * k, o);
+                    SplitRows<D>::store(smem, row, o, 32 * k);
+                }
+                *reinterpret_cast<float2*>(smem + SplitRows<D>::kMl + row * 8) = make_float2(m, l);
+            }
+        } else if (ok) {
             tc_fence_after();
             const float inv = 1.f / l;
             uint8_t* mine = smem + row * kRowStride;
@@ -527,8 +561,18 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
                                    float2_to_bf16x2(o[8 * q + 6] * inv, o[8 * q + 7] * inv));
             }
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // the softmax warps: rows staged
-        if (!*abort) {
+        if (SPLIT && s_ranks > 1) {
+            __syncwarp();
+            cluster_sync();  // every rank's rows are staged
+            SplitRows<D>::join(smem, s_ranks, nrows - row0 < Cfg::kBM ? nrows - row0 : Cfg::kBM, threadIdx.x,
+                               [&](int rr) {
+                                   const int rg = row0 + rr;
+                                   return p.out + ((int64_t(q0) + rg / G) * p.Hq + g * G + rg % G) * D;
+                               });
+        } else {
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // the softmax warps: rows staged
+        }
+        if (!*abort && !(SPLIT && s_ranks > 1)) {
             constexpr int kChunks = D / 8, kRowsPerPass = 32 / kChunks;
             for (int rr = warp * kRowsPerPass + lane / kChunks; rr < Cfg::kBM; rr += 4 * kRowsPerPass) {
                 const int rg = row0 + rr;
@@ -539,6 +583,12 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
                 reinterpret_cast<uint4*>(p.out + grow * D)[ch] = v;
             }
         }
+    }
+
+    if (SPLIT && s_ranks > 1) {
+        __syncwarp();
+        if (warp >= 4) cluster_sync();
+        cluster_sync();  // every rank's rows are read
     }
 
     // ---- release TMEM once every warp's tcgen05 work has finished ----

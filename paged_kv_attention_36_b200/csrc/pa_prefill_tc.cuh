@@ -62,9 +62,9 @@ namespace pa {
 // wave took 9 % of the time) and a sequence's pages are read close together.
 struct TileOfCta {
     int b, tile, g;
-    __device__ __forceinline__ TileOfCta(const PrefillParams& p) {
-        const int r = int(blockIdx.x) / p.Hkv, lane = threadIdx.x & 31;
-        g = int(blockIdx.x) - r * p.Hkv;
+    __device__ __forceinline__ TileOfCta(const PrefillParams& p, int cta) {
+        const int r = cta / p.Hkv, lane = threadIdx.x & 31;
+        g = cta - r * p.Hkv;
         b = r / p.tiles_per_seq;
         tile = p.tiles_per_seq - 1 - (r - b * p.tiles_per_seq);
         if (p.B <= 32) {
@@ -75,6 +75,85 @@ struct TileOfCta {
                 longer += other > mine || (other == mine && i < lane);
             }
             b = __ffs(__ballot_sync(0xffffffffu, lane < p.B && longer == b)) - 1;
+        }
+    }
+};
+
+// Few rows over long contexts: the CTAs of a cluster share a tile, each taking a
+// run of its key blocks (at least kSplitMinBlocks, so that what the join costs,
+// about 1.5 us, stays below what it saves), and meet in one another's shared
+// memory: no workspace, no second kernel.  Rank r's run starts at block r * per;
+// ranks past the last run leave at once.  Measured, bf16 and 8-bit cache: one
+// token, 32/8 heads of 128, over 16,000: 238 and 356 us by one CTA a tile, 40 and
+// 64 us by 8, 29 and 45 us by 16.  Runs of 2 blocks or more: 8 rows over 256 tokens
+// 10.7 and 13.2 us in place of 9.3 and 11.9, over 512 11.7 and 13.7 in place of
+// 12.8 and 15.7.
+constexpr int kSplitMinBlocks = 4, kMaxRanks = 16;
+struct KeySplit {
+    int ranks, per;  // CTAs that have blocks, blocks of each but the last
+    __device__ __forceinline__ explicit KeySplit(int nblk) {
+        const int n = int(cluster_size());
+        per = (nblk + n - 1) / n;
+        if (per < kSplitMinBlocks) per = kSplitMinBlocks;
+        ranks = (nblk + per - 1) / per;
+    }
+};
+
+// A split tile's rows in shared memory: 128 rows of D fp32 sums, padded by 16
+// bytes, then (m, l) of each row, then the weights of each rank in the rows that
+// this CTA joins.
+template <int D>
+struct SplitRows {
+    static constexpr int kStride = D * 4 + 16, kMl = 128 * kStride, kW = kMl + 128 * 8, kBytes = kW + 128 * 4 * kMaxRanks;
+    // O columns [first, first + 32) of row
+    static __device__ __forceinline__ void store(uint8_t* smem, int row, const float* o, int first) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(smem + row * kStride + (first + i) * 4) =
+                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    }
+    // The calling 128 threads (tid, barrier 1) write this rank's share of the
+    // tile's first nrows rows, in rank order:
+    // out[r] = sum_i w_i O_i, w_i = 2^(m_i - M) / sum_j 2^(m_j - M) l_j, M = max m_i.
+    // w_i is 0 for a rank whose keys the row does not see (m_i = -inf, O_i = 0).
+    template <class Out>
+    static __device__ __forceinline__ void join(uint8_t* smem, int ranks, int nrows, int tid, Out out) {
+        const int share = (128 + ranks - 1) / ranks, r0 = int(cluster_rank()) * share;
+        const int n = nrows - r0 < share ? nrows - r0 : share;
+        const uint32_t base = smem_u32(smem);
+        float* w = reinterpret_cast<float*>(smem + kW);
+        if (tid < n) {
+            float M = -INFINITY, L = 0.f;
+#pragma unroll 1
+            for (int i = 0; i < ranks; ++i) {
+                const float2 ml = ld_cluster_f2(cluster_addr(base, i) + kMl + (r0 + tid) * 8);
+                const float top = fmaxf(M, ml.x);
+                // 0 * exp2(-inf) until the first rank that sees a key
+                L = (M == -INFINITY ? 0.f : L * exp2f(M - top)) + (ml.x == -INFINITY ? 0.f : exp2f(ml.x - top) * ml.y);
+                M = top;
+                w[tid * kMaxRanks + i] = ml.x;
+            }
+            const float inv = 1.f / L;
+#pragma unroll 1
+            for (int i = 0; i < ranks; ++i) w[tid * kMaxRanks + i] = exp2f(w[tid * kMaxRanks + i] - M) * inv;
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        constexpr int kChunks = D / 4;
+        for (int x = tid; x < n * kChunks; x += 128) {
+            const int row = x / kChunks, ch = x % kChunks;
+            const uint32_t a = base + (r0 + row) * kStride + ch * 16;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int i = 0; i < ranks; ++i) {
+                const float4 o = ld_cluster_f4(cluster_addr(a, i));
+                const float wi = w[row * kMaxRanks + i];
+                s.x += wi * o.x;
+                s.y += wi * o.y;
+                s.z += wi * o.z;
+                s.w += wi * o.w;
+            }
+            *reinterpret_cast<uint2*>(out(r0 + row) + ch * 4) =
+                make_uint2(float2_to_bf16x2(s.x, s.y), float2_to_bf16x2(s.z, s.w));
         }
     }
 };
@@ -112,9 +191,11 @@ struct TcPrefillCfg {
 // sees are streamed, as one list: `ns` pages of sinks, then the pages from the
 // first row's window on, `skip` pages between them left out.  A row sees list
 // keys [0, min(sinks, hi)) and [lo, hi).  Measured: 16 chunks of 512 tokens,
-// window 1024, 4 sinks, 32/8 heads of 64: 124.5 us, 467 TFLOP/s of visible pairs
+// window 1024, 4 sinks, 32/8 heads of 64: 122.1 us, 477 TFLOP/s of visible pairs
 // (blocks of 64 keys at the window's edges are multiplied whole).
-template <bool PREFIX, int D, int G, int BN, int KS, int NS, bool WINDOW = false, class Params>
+// SPLIT (WINDOW): a cluster of CTAs on each tile (KeySplit).  A kernel of its own:
+// the same code in the unsplit one costs it registers (127 against 122 us above).
+template <bool PREFIX, int D, int G, int BN, int KS, int NS, bool WINDOW = false, bool SPLIT = false, class Params>
 __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     using Cfg = TcPrefillCfg<D, BN, KS, NS>;
     static_assert(Cfg::kBM % G == 0, "a tile holds whole tokens (members)");
@@ -132,7 +213,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     uint64_t* p_full = s_full + NS;
     uint64_t* drain = p_full + NS;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_ranks;  // s_ranks (SPLIT): CTAs that share the tile
     volatile int* abort = &s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int g = blockIdx.y;
@@ -141,12 +222,14 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     int nrows, row0, nkeys;  // rows of the task, the tile's first row, keys staged (0 .. nkeys-1)
     const int32_t* bt;       // block-table entries of the staged pages
     int L = 0, q0 = 0, first_pos = 0, first = 0, P = 0, pg0 = 0;
-    int ns = 0, skip = 0, f0 = 0;  // WINDOW: f0 = list key of the first row's first window token
+    int ns = 0, skip = 0, sinks = 0;
+    int f0 = 0;  // WINDOW: f0 = list key of the first row's first window token
+    int shift = 0;                 // WINDOW: tokens before list key 0, or left out before the window
     if constexpr (!PREFIX) {
         int b = int(blockIdx.x) / p.tiles_per_seq;
         int tile = int(blockIdx.x) - b * p.tiles_per_seq;
         if constexpr (WINDOW) {
-            const TileOfCta mine(p);
+            const TileOfCta mine(p, int(SPLIT ? blockIdx.x / cluster_size() : blockIdx.x));
             b = mine.b;
             tile = mine.tile;
             g = mine.g;
@@ -176,8 +259,9 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
             const WindowPages w(f0, nkeys, p.sinks);
             ns = w.ns;
             skip = w.skip;
-            f0 -= skip * 16;
-            nkeys -= skip * 16;
+            shift = skip * 16;
+            f0 -= shift;
+            nkeys -= shift;
         }
         bt = p.block_tables + int64_t(b) * p.M;
     } else {
@@ -205,8 +289,26 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         nkeys = (pg1 - pg0) * 16;  // shared pages are whole
         bt = p.block_tables + int64_t(first) * p.M + pg0;  // the group leader's table
     }
-    const int pages = (nkeys + 15) / 16;
-    const int nblk = (nkeys + BN - 1) / BN;
+    int pages = (nkeys + 15) / 16;
+    int nblk = (nkeys + BN - 1) / BN;
+    if constexpr (WINDOW) sinks = p.sinks;
+    if constexpr (SPLIT) {
+        const KeySplit split(nblk);
+        const int rank = int(cluster_rank());
+        if (rank >= split.ranks) return;  // before any barrier or TMEM use
+        if (threadIdx.x == 0) s_ranks = split.ranks;
+        // the list from this rank's first block on: pages, keys and sinks count from there
+        const int first_pg = rank * split.per * Cfg::kPages;
+        bt += first_pg;
+        ns -= first_pg;
+        shift += first_pg * 16;
+        nkeys -= first_pg * 16;
+        sinks -= first_pg * 16;
+        f0 -= first_pg * 16;
+        pages -= first_pg;
+        if (pages > split.per * Cfg::kPages) pages = split.per * Cfg::kPages;
+        nblk = (pages + Cfg::kPages - 1) / Cfg::kPages;
+    }
 
     // Loads in flight while the barriers and TMEM are set up: the page ids of
     // block 0 (producer lanes) and this thread's Q row (softmax warps).
@@ -377,12 +479,11 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         // keys 0 .. lim-1 are visible to this row; its query row
         // (WINDOW: keys [0, sink) and [lo, lim) of the list; rows past the task as its last one)
         const int pos1 = first_pos + r / G + 1;  // the row's position + 1
-        const int lim = PREFIX ? nkeys : WINDOW ? (valid ? pos1 - skip * 16 : nkeys) : (valid ? pos1 : 1);
+        const int lim = PREFIX ? nkeys : WINDOW ? (valid ? pos1 - shift : nkeys) : (valid ? pos1 : 1);
         int lo = 0, sink = 0;
         if constexpr (WINDOW) {
-            const int from = window_first(lim - 1 + skip * 16, p.window);
-            lo = from - skip * 16;
-            sink = p.sinks < lim ? p.sinks : lim;
+            lo = window_first(lim - 1 + shift, p.window) - shift;
+            sink = sinks < lim ? sinks : lim;
         }
         const int64_t qrow = int64_t(PREFIX ? first : q0) + r / G;
 
@@ -493,8 +594,8 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
             if constexpr (WINDOW) {
                 // V rows of the list that no row of the tile sees: between the
                 // sinks and the first window, and past the context
-                const int gap = p.sinks > n0 ? p.sinks : n0, gap_end = f0 < n0 + BN ? f0 : n0 + BN;
-                const int past = L - skip * 16 > n0 ? L - skip * 16 : n0;
+                const int gap = sinks > n0 ? sinks : n0, gap_end = f0 < n0 + BN ? f0 : n0 + BN;
+                const int past = L - shift > n0 ? L - shift : n0;
                 const int past_end = pages * 16 < n0 + BN ? pages * 16 : n0 + BN;
                 if (gap < gap_end || past < past_end) {
                     ok = __all_sync(0xffffffffu, mbar_wait_sleep(&v_full[j % KS], uint32_t(j / KS) & 1, abort));
@@ -535,7 +636,19 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         constexpr int kRowBytes = D * (PREFIX ? 4 : 2);
         constexpr int kRowStride = kRowBytes + 16;
         static_assert(Cfg::kBM * kRowStride <= Cfg::kBarOff, "output staging fits in the Q and ring space");
-        if (ok) {
+        if (SPLIT && s_ranks > 1) {
+            if (ok) {  // this rank's sums, for the cluster
+                static_assert(SplitRows<D>::kBytes <= Cfg::kBarOff, "split staging fits in the Q and ring space");
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[32];
+                    tmem_ld32(t_o + lanes + 32 * k, o);
+                    SplitRows<D>::store(smem, row, o, 32 * k);
+                }
+                *reinterpret_cast<float2*>(smem + SplitRows<D>::kMl + row * 8) = make_float2(m, l);
+            }
+        } else if (ok) {
             tc_fence_after();
             const float inv = 1.f / l;
             uint8_t* mine = smem + row * kRowStride;
@@ -563,8 +676,21 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
                 if (valid) p.prefix_ml[(int64_t(blockIdx.z) * p.B + qrow) * p.Hq + g * G + r % G] = make_float2(m, l);
             }
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");  // the 4 softmax warps: rows staged
-        if (!*abort) {
+        bool whole = true;  // this CTA holds the tile's sums
+        if constexpr (SPLIT) {
+            whole = s_ranks == 1;
+            if (!whole) {
+                __syncwarp();
+                cluster_sync();  // every rank's rows are staged
+                SplitRows<D>::join(smem, s_ranks, nrows - row0 < Cfg::kBM ? nrows - row0 : Cfg::kBM,
+                                   (warp - 2) * 32 + lane, [&](int rr) {
+                                       const int rg = row0 + rr;
+                                       return p.out + ((int64_t(q0) + rg / G) * p.Hq + g * G + rg % G) * D;
+                                   });
+            }
+        }
+        if (whole) asm volatile("bar.sync 1, 128;" ::: "memory");  // the 4 softmax warps: rows staged
+        if (!*abort && whole) {
             constexpr int kChunks = kRowBytes / 16;       // 16-byte chunks per row
             constexpr int kRowsPerPass = 32 / kChunks;    // rows per warp instruction
             const int wq = warp - 2;
@@ -602,6 +728,14 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         }
     }
 
+    if constexpr (SPLIT) {
+        if (s_ranks > 1) {
+            __syncwarp();
+            if (warp < 2) cluster_sync();
+            cluster_sync();  // every rank's rows are read
+        }
+    }
+
     // ---- release TMEM once every warp's tcgen05 work has finished ----
     tc_fence_before();
     __syncthreads();
@@ -611,9 +745,13 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     }
 }
 
-template <int D, int G, int BN, int KS, int CPS, int NS, bool WINDOW = false>
+template <int D, int G, int BN, int KS, int CPS, int NS, bool WINDOW = false, bool SPLIT = false>
 __global__ void __launch_bounds__(6 * 32, CPS) prefill_tc_kernel(const __grid_constant__ PrefillParams p) {
-    tc_attention_tile<false, D, G, BN, KS, NS, WINDOW>(p);
+    if constexpr (WINDOW) {  // launched as a programmatic dependent
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+    }
+    tc_attention_tile<false, D, G, BN, KS, NS, WINDOW, SPLIT>(p);
 }
 
 // The shared-prefix (cascade) pass on tcgen05: grid (group x row tile, kv

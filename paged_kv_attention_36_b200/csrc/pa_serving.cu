@@ -96,18 +96,24 @@ pa_status by_shape(const pa_dims& d, F fn) {
 
 // Launches with programmatic serialization: the kernel's set-up may overlap
 // the end of the one before it (it waits with griddepcontrol.wait).
+// `cluster` CTAs (along x) form a cluster.
 template <class Kernel, class Params>
-pa_status launch_dependent(Kernel kern, dim3 grid, int threads, int smem, cudaStream_t stream, const Params& p) {
+pa_status launch_dependent(Kernel kern, dim3 grid, int threads, int smem, cudaStream_t stream, const Params& p,
+                           unsigned cluster = 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(unsigned(threads));
     cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return PA_ERR_CUDA;
     return launched();
 }
@@ -178,38 +184,66 @@ pa_status decode_wide(const Call& c, void* workspace, size_t workspace_bytes, vo
     return by_shape(*c.dims, DecodeWide<I8>{p, grid, static_cast<cudaStream_t>(stream)});
 }
 
+// CTAs that share a tile's key blocks: two while they fit two per SM, more (to
+// kMaxRanks) while they fit one per SM, as long as the longest row that the tables
+// and the window allow gives each its blocks.  The lengths are on the device, so
+// wide tables cost short contexts the larger launch.  Measured without and with
+// it, bf16 and 8-bit cache, 32/8 heads of 128: one token over 16,000 tokens 238
+// and 356 -> 29 and 45 us; 16 sequences of 4 rows over 2,000 38 and 66 -> 31 and
+// 45 us; heads of 64 over 60 tokens of 65,536 possible 6.3 and 7.2 -> 8.2 and 9.7
+// us.  Two per SM beyond two ranks: 16.8 in place of 14.6 us for 8 sequences of 16
+// rows over 500 tokens (13.1 us unsplit), 13.5 in place of 14.7 us over 1,000.
+unsigned key_cluster(const Call& c, unsigned tiles) {
+    const pa_dims& d = *c.dims;
+    int64_t keys = int64_t(d.max_blocks_per_seq) * kBlockSize;
+    const int64_t seen = int64_t(c.window) + c.sinks + c.max_q_len;
+    if (seen < keys) keys = seen;
+    const int64_t blocks = (keys + 63) / 64, sms = sm_count();
+    unsigned n = 1;
+    while (n < pa::kMaxRanks && int64_t(tiles) * n * 2 <= (n == 1 ? 2 * sms : sms) &&
+           blocks >= int64_t(n) * 2 * pa::kSplitMinBlocks)
+        n *= 2;
+    return n;
+}
+
 struct PrefillWindow {
     const pa::PrefillParams& p;
-    dim3 grid;
+    unsigned tiles, cluster;
     cudaStream_t stream;
+    template <int D, int G, bool SPLIT>
+    pa_status run() const {
+        using S = TcShape<D, 64>;
+        auto kern = pa::prefill_tc_kernel<D, G, 64, S::KS, S::CPS, S::NS, true, SPLIT>;
+        static unsigned attr_done[kMaxDevices];
+        if (!set_smem_once(kern, S::Cfg::kSmemBytes, attr_done, SPLIT)) return PA_ERR_CUDA;
+        return launch_dependent(kern, dim3(tiles * cluster), S::Cfg::kThreads, S::Cfg::kSmemBytes, stream, p, cluster);
+    }
     template <int D, int G>
     pa_status operator()() const {
-        using S = TcShape<D, 64>;
-        auto kern = pa::prefill_tc_kernel<D, G, 64, S::KS, S::CPS, S::NS, true>;
-        static unsigned attr_done[kMaxDevices];
-        if (!set_smem_once(kern, S::Cfg::kSmemBytes, attr_done)) return PA_ERR_CUDA;
-        kern<<<grid, S::Cfg::kThreads, S::Cfg::kSmemBytes, stream>>>(p);
-        return launched();
+        return cluster > 1 ? run<D, G, true>() : run<D, G, false>();
     }
 };
 
 struct PrefillI8 {
     const pa::PrefillI8Params& p;
-    dim3 grid;
+    unsigned tiles, cluster;
     cudaStream_t stream;
-    template <int D, int G>
-    pa_status operator()() const {
+    template <int D, int G, bool SPLIT>
+    pa_status run() const {
         using Cfg = pa::I8PrefillCfg<D>;
-        auto kern = pa::prefill_i8_kernel<D, G>;
+        auto kern = pa::prefill_i8_kernel<D, G, SPLIT>;
         // the kernel's setmaxnreg split needs exactly the registers it counts on
         static const bool regs_ok = [&] {
             cudaFuncAttributes a;
             return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == Cfg::kRegs;
         }();
         static unsigned attr_done[kMaxDevices];
-        if (!regs_ok || !set_smem_once(kern, Cfg::kSmemBytes, attr_done)) return PA_ERR_CUDA;
-        kern<<<grid, Cfg::kThreads, Cfg::kSmemBytes, stream>>>(p);
-        return launched();
+        if (!regs_ok || !set_smem_once(kern, Cfg::kSmemBytes, attr_done, SPLIT)) return PA_ERR_CUDA;
+        return launch_dependent(kern, dim3(tiles * cluster), Cfg::kThreads, Cfg::kSmemBytes, stream, p, cluster);
+    }
+    template <int D, int G>
+    pa_status operator()() const {
+        return cluster > 1 ? run<D, G, true>() : run<D, G, false>();
     }
 };
 
@@ -373,8 +407,8 @@ pa_status pa_prefill_window(const void* q, const int32_t* cu_q_lens, int32_t max
         !make_panel_map(&p.tmap_v, v_cache, cache_tiles, d.head_dim, d.block_size))
         return PA_ERR_CUDA;
     fill_prefill(c, p);
-    const dim3 grid(unsigned(d.num_seqs * p.tiles_per_seq * d.num_kv_heads));
-    return by_shape(d, PrefillWindow{p, grid, static_cast<cudaStream_t>(stream)});
+    const unsigned tiles = unsigned(d.num_seqs * p.tiles_per_seq * d.num_kv_heads);
+    return by_shape(d, PrefillWindow{p, tiles, key_cluster(c, tiles), static_cast<cudaStream_t>(stream)});
 }
 
 pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_len, const void* k_cache,
@@ -393,8 +427,8 @@ pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_l
     p.v_cache = static_cast<const int8_t*>(v_cache);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    const dim3 grid(unsigned(dims->num_seqs * p.a.tiles_per_seq * dims->num_kv_heads));
-    return by_shape(*dims, PrefillI8{p, grid, static_cast<cudaStream_t>(stream)});
+    const unsigned tiles = unsigned(dims->num_seqs * p.a.tiles_per_seq * dims->num_kv_heads);
+    return by_shape(*dims, PrefillI8{p, tiles, key_cluster(c, tiles), static_cast<cudaStream_t>(stream)});
 }
 
 pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,

@@ -198,6 +198,30 @@ def test_prefill_i8(pa, window, sinks, Hq, Hkv, D):
         ref.assert_attention(out[rows], want, mean_abs, PREFILL_WEIGHTS)
 
 
+@pytest.mark.parametrize("window,sinks", [(ref.ALL, 0), (700, 0), (300, 600), (2400, 4)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 1, 128), (8, 1, 64), (3, 3, 128)])
+def test_prefill_i8_few_rows_long_contexts(pa, window, sinks, Hq, Hkv, D):
+    # a tile's keys are shared by the CTAs of a cluster; some have no key that a row sees
+    g = torch.Generator().manual_seed(window % 1000 + sinks + D)
+    q_lens = [1, 3, 0, 20, 129, 2]
+    lens = [4001, 2500, 7, 257, 1100, 513]
+    k, v, ks, vs, bt = ref.i8_batch(g, lens, Hkv, D)
+    q = torch.randn((sum(q_lens), Hq, D), generator=g).bfloat16()
+    cu = torch.tensor([0] + torch.tensor(q_lens).cumsum(0).tolist(), dtype=torch.int32)
+    args = (q.cuda(), cu.cuda(), max(q_lens), k.cuda(), v.cuda(), ks.cuda(), vs.cuda(), bt.cuda(),
+            torch.tensor(lens, dtype=torch.int32).cuda(), D ** -0.5)
+    out = torch.full_like(q, float("nan")).cuda()
+    pa.pa_prefill_i8(*args, out, window=window, sinks=sinks)
+    assert pa.pa_device_errors(clear=True) == 0
+    for b, n in enumerate(lens):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        want, mean_abs = ref.attend(q[rows], *ref.values_i8(k, v, ks, vs, bt[b], n), D ** -0.5, window, sinks)
+        ref.assert_attention(out[rows], want, mean_abs, PREFILL_WEIGHTS)
+    again = torch.full_like(out, float("nan"))
+    pa.pa_prefill_i8(*args, again, window=window, sinks=sinks)
+    assert torch.equal(again, out), "repeated calls differ"
+
+
 def test_prefill_i8_scales_far_apart(pa):
     g = torch.Generator().manual_seed(22)
     k, v, ks, vs, bt = ref.i8_batch(g, [400], 2, 64)

@@ -163,6 +163,35 @@ def test_prefill_window_head_layouts(pa):
             ref.assert_attention(out[rows], want, mean_abs, 2.0 ** -8)
 
 
+@pytest.mark.parametrize("window,sinks", [(ref.ALL, 0), (700, 0), (1500, 100), (300, 600), (60, 2000), (2400, 4)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(2, 1, 128), (8, 1, 64), (3, 3, 128)])
+def test_prefill_window_few_rows_long_contexts(pa, window, sinks, Hq, Hkv, D):
+    # a tile's keys are shared by the CTAs of a cluster; some have no key that a row sees
+    g = torch.Generator().manual_seed(window % 1000 + sinks + D)
+    q_lens = [1, 3, 0, 20, 129, 2]
+    lens = [4001, 2500, 7, 257, 1100, 513]
+    ks, vs, kp, vp, bt = ref.bf16_batch(g, lens, Hkv, D)
+    kp, vp, bt = _forget(kp, vp, bt, lens, [n - c for n, c in zip(lens, q_lens)], window, sinks)
+    q = torch.randn((sum(q_lens), Hq, D), generator=g).bfloat16()
+    cu = torch.tensor([0] + torch.tensor(q_lens).cumsum(0).tolist(), dtype=torch.int32)
+    out = torch.full_like(q, float("nan")).cuda()
+    args = (q.cuda(), cu.cuda(), max(q_lens), kp.cuda(), vp.cuda(), bt.cuda(),
+            torch.tensor(lens, dtype=torch.int32).cuda(), D ** -0.5)
+    pa.pa_prefill_window(*args, out, window=window, sinks=sinks)
+    assert pa.pa_device_errors(clear=True) == 0
+    for b, n in enumerate(lens):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        want, mean_abs = ref.attend(q[rows], ks[b].double(), vs[b].double(), D ** -0.5, window, sinks)
+        ref.assert_attention(out[rows], want, mean_abs, 2.0 ** -8)
+    again = torch.full_like(out, float("nan"))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_prefill_window(*args, again, window=window, sinks=sinks)
+        pa.pa_prefill_window(*args, again, window=window, sinks=sinks)
+    graph.replay()
+    assert torch.equal(again, out), "a replayed call differs"
+
+
 def test_window_device_errors(pa):
     # a bad block id inside the window is reported; one outside it is never read
     g = torch.Generator().manual_seed(6)
