@@ -85,7 +85,7 @@ struct TileOfCta {
 // memory: no workspace, no second kernel.  Rank r's run starts at block r * per;
 // ranks past the last run leave at once.  Measured, bf16 and 8-bit cache: one
 // token, 32/8 heads of 128, over 16,000: 238 and 356 us by one CTA a tile, 40 and
-// 64 us by 8, 29 and 45 us by 16.  Runs of 2 blocks or more: 8 rows over 256 tokens
+// 64 us by 8, 29 and 45 us by 16.  With CTAs two to an SM, runs of 2 blocks or more: 8 rows over 256 tokens
 // 10.7 and 13.2 us in place of 9.3 and 11.9, over 512 11.7 and 13.7 in place of
 // 12.8 and 15.7.
 constexpr int kSplitMinBlocks = 4, kMaxRanks = 16;

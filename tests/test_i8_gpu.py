@@ -222,6 +222,25 @@ def test_prefill_i8_few_rows_long_contexts(pa, window, sinks, Hq, Hkv, D):
     assert torch.equal(again, out), "repeated calls differ"
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_prefill_i8_few_rows_nonfinite_scale_reaches_who_sees_it(pa, D, which, bad):
+    # windows of rows 0, 1, 2 start at tokens 1998, 1999, 2000; the block of 1984-1999 has a bad scale
+    g = torch.Generator().manual_seed(D)
+    k, v, ks, vs, bt = ref.i8_batch(g, [3000], 2, D)
+    q = torch.randn((3, 4, D), generator=g).bfloat16()
+    want, mean_abs = ref.attend(q, *ref.values_i8(k, v, ks, vs, bt[0], 3000), D ** -0.5, 1000, 0)
+    (ks if which == "k" else vs)[int(bt[0, 1999 // 16])] = bad
+    out = torch.zeros_like(q).cuda()
+    pa.pa_prefill_i8(q.cuda(), torch.tensor([0, 3], dtype=torch.int32).cuda(), 3, k.cuda(), v.cuda(), ks.cuda(),
+                     vs.cuda(), bt.cuda(), torch.tensor([3000], dtype=torch.int32).cuda(), D ** -0.5, out,
+                     window=1000, sinks=0)
+    if bad != bad:
+        assert torch.isnan(out[:2]).all(), "a NaN scale was dropped"
+    ref.assert_attention(out[2:], want[2:], mean_abs[2:], PREFILL_WEIGHTS)
+
+
 def test_prefill_i8_scales_far_apart(pa):
     g = torch.Generator().manual_seed(22)
     k, v, ks, vs, bt = ref.i8_batch(g, [400], 2, 64)

@@ -192,6 +192,23 @@ def test_prefill_window_few_rows_long_contexts(pa, window, sinks, Hq, Hkv, D):
     assert torch.equal(again, out), "a replayed call differs"
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_window_few_rows_nan_key_reaches_who_sees_it(pa, D):
+    # windows of rows 0, 1, 2 start at tokens 1998, 1999, 2000; key 1999 is NaN
+    g = torch.Generator().manual_seed(D)
+    ks, vs, kp, vp, bt = ref.bf16_batch(g, [3000], 2, D)
+    blk = int(bt[0, 1999 // 16])
+    q = torch.randn((3, 4, D), generator=g).bfloat16()
+    args = (bt.cuda(), torch.tensor([3000], dtype=torch.int32).cuda(), D ** -0.5)
+    kp[blk, :, 1999 % 16] = float("nan")
+    out = torch.zeros_like(q).cuda()
+    pa.pa_prefill_window(q.cuda(), torch.tensor([0, 3], dtype=torch.int32).cuda(), 3, kp.cuda(), vp.cuda(), *args, out,
+                         window=1000, sinks=0)
+    assert torch.isnan(out[:2]).all(), "a NaN key was dropped"
+    want, mean_abs = ref.attend(q, ks[0].double(), vs[0].double(), D ** -0.5, 1000, 0)
+    ref.assert_attention(out[2:], want[2:], mean_abs[2:], 2.0 ** -8)
+
+
 def test_window_device_errors(pa):
     # a bad block id inside the window is reported; one outside it is never read
     g = torch.Generator().manual_seed(6)
