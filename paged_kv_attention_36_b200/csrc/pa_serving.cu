@@ -195,12 +195,12 @@ pa_status decode_wide(const Call& c, void* workspace, size_t workspace_bytes, vo
 // 45 us; heads of 64 over 60 tokens of 65,536 possible 6.3 and 7.2 -> 8.2 and 9.7
 // us.  Two per SM beyond two ranks: 16.8 in place of 14.6 us for 8 sequences of 16
 // rows over 500 tokens (13.1 us unsplit), 13.5 in place of 14.7 us over 1,000.
-unsigned key_cluster(const Call& c, unsigned tiles) {
+unsigned key_cluster(const Call& c, unsigned tiles, int64_t sms) {
     const pa_dims& d = *c.dims;
     int64_t keys = int64_t(d.max_blocks_per_seq) * kBlockSize;
     const int64_t seen = int64_t(c.window) + c.sinks + c.max_q_len;
     if (seen < keys) keys = seen;
-    const int64_t blocks = (keys + 63) / 64, sms = sm_count();
+    const int64_t blocks = (keys + 63) / 64;
     unsigned n = 1;
     while (n < pa::kMaxRanks && int64_t(tiles) * n * 2 <= (n == 1 ? 2 * sms : sms) &&
            blocks >= int64_t(n) * 2 * pa::kSplitMinBlocks)
@@ -385,13 +385,12 @@ pa_status launch_rope(const pa::RopeParams& p, cudaStream_t s) {
 }
 
 template <int D, int HP>
-pa_status launch_rope_i8(pa::RopeParams& p, cudaStream_t s) {
+pa_status launch_rope_i8(pa::RopeParams& p, int sms, cudaStream_t s) {
     const int64_t items = int64_t(p.T) * ((p.Hq + HP - 1) / HP) * (D / 16);
     if (items >= int64_t(1) << 32) return PA_ERR_SHAPE;
     // a decode step's tokens have a block each and a CTA each (128 tokens: 4.9 us,
     // 31.9 us with 16 to a CTA); of a long call's tokens few are their block's
     // first, and a CTA looks at up to 16 (7295 tokens: 56.7 us, 59.4 us with one)
-    const int sms = sm_count();
     p.tokens_per_cta = p.T <= 4 * sms ? 1 : p.T / (4 * sms) < 16 ? p.T / (4 * sms) : 16;
     // a tile per warp: as many CTAs as a block's tiles need, while there are SMs
     // for them (128 tokens, 8 kv heads: 4.9 us, 6.6 us with two tiles a warp)
@@ -411,9 +410,11 @@ pa_status append_i8(const Append& a, cudaStream_t s) {
     pa::RopeParams p;
     const pa_status st = prepare_append(a, true, p);
     if (st != PA_OK || p.T == 0) return st;
-    const bool many = rows_in_fours(int64_t(p.T) * p.Hq, p.D, sm_count());  // in twos here: four leave too few registers
-    if (p.D == 64) return many ? launch_rope_i8<64, 2>(p, s) : launch_rope_i8<64, 1>(p, s);
-    return many ? launch_rope_i8<128, 2>(p, s) : launch_rope_i8<128, 1>(p, s);
+    const int sms = sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    const bool many = rows_in_fours(int64_t(p.T) * p.Hq, p.D, sms);  // in twos here: four leave too few registers
+    if (p.D == 64) return many ? launch_rope_i8<64, 2>(p, sms, s) : launch_rope_i8<64, 1>(p, sms, s);
+    return many ? launch_rope_i8<128, 2>(p, sms, s) : launch_rope_i8<128, 1>(p, sms, s);
 }
 
 }  // namespace
@@ -445,6 +446,8 @@ pa_status pa_prefill_window(const void* q, const int32_t* cu_q_lens, int32_t max
     bool done;
     const pa_status st = check_prefill(c, &done);
     if (st != PA_OK || done) return st;
+    const int sms = sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
     const pa_dims& d = *dims;
     pa::PrefillParams p;
     const int64_t cache_tiles = int64_t(d.num_blocks) * d.num_kv_heads;
@@ -453,7 +456,7 @@ pa_status pa_prefill_window(const void* q, const int32_t* cu_q_lens, int32_t max
         return PA_ERR_CUDA;
     fill_prefill(c, p);
     const unsigned tiles = unsigned(d.num_seqs * p.tiles_per_seq * d.num_kv_heads);
-    return by_shape(d, PrefillWindow{p, tiles, key_cluster(c, tiles), static_cast<cudaStream_t>(stream)});
+    return by_shape(d, PrefillWindow{p, tiles, key_cluster(c, tiles, sms), static_cast<cudaStream_t>(stream)});
 }
 
 pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_len, const void* k_cache,
@@ -466,6 +469,8 @@ pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_l
     pa_status st = check_prefill(c, &done);
     if (st != PA_OK || done) return st;
     if ((st = scales_ok(c)) != PA_OK) return st;
+    const int sms = sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
     pa::PrefillI8Params p{};
     fill_prefill(c, p.a);
     p.k_cache = static_cast<const int8_t*>(k_cache);
@@ -473,7 +478,7 @@ pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_l
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     const unsigned tiles = unsigned(dims->num_seqs * p.a.tiles_per_seq * dims->num_kv_heads);
-    return by_shape(*dims, PrefillI8{p, tiles, key_cluster(c, tiles), static_cast<cudaStream_t>(stream)});
+    return by_shape(*dims, PrefillI8{p, tiles, key_cluster(c, tiles, sms), static_cast<cudaStream_t>(stream)});
 }
 
 pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
@@ -484,8 +489,10 @@ pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k_new, int
                                                num_tokens, q_out, k_cache, v_cache, nullptr, nullptr, dims},
                                         false, p);
     if (st != PA_OK || p.T == 0) return st;
+    const int sms = sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return rows_in_fours(int64_t(p.T) * (p.Hq + 2 * p.Hkv), p.D, sm_count()) ? launch_rope<4>(p, s) : launch_rope<1>(p, s);
+    return rows_in_fours(int64_t(p.T) * (p.Hq + 2 * p.Hkv), p.D, sms) ? launch_rope<4>(p, s) : launch_rope<1>(p, s);
 }
 
 pa_status pa_rope_append_i8(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
