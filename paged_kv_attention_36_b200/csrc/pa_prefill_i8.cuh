@@ -15,7 +15,7 @@
 //     which the softmax's fma takes away with the page's K scale.
 //   * V stays transposed: its tile rows are head_dim, so a block is the
 //     K-major B operand [D][64 tokens] of P V.
-//   * Queries are scaled by a power of two to below 2 in f16, which loses
+//   * Queries are scaled by a power of two to below 4 in f16, which loses
 //     nothing bf16 holds down to 2^-14 of the row's largest value.
 //   * Scales cost no work per value: with c = scale * log2(e) * k_scale of
 //     the page and v = log2(v_scale), P = 2^(s c + (v - m - bias c)) is the
@@ -392,8 +392,10 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
                     top = fmax3(top, fabsf(f.x), fabsf(f.y));
                 }
             }
-            const int e = top > 0.f && top < INFINITY ? ilogbf(top) : 0;
-            const float down = exp2f(float(-e));
+            // v * down is exact and below 4, whatever finite values the row has
+            int e = int(__float_as_uint(top) >> 23) - 127;
+            e = e < -126 ? -126 : e > 126 ? 126 : e;
+            const float down = __uint_as_float(uint32_t(127 - e) << 23);
 #pragma unroll
             for (int ch = 0; ch < D / 8; ++ch) {
                 uint32_t w[4] = {qv[ch].x, qv[ch].y, qv[ch].z, qv[ch].w};
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
             }
             fence_proxy_async_smem();
             mbar_arrive(q_full);
-            ce = p.qscale * exp2f(float(e));
+            ce = p.qscale * __uint_as_float(uint32_t(127 + e) << 23);
             bias = 1152.f * sum;
         }
         const bool positive = ce > 0.f;
@@ -428,10 +430,9 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
             ks_next = __ldg(pp.k_scale + tl_next);
             vs_next = __ldg(pp.v_scale + tl_next);
             tl_next = page_tile(j + 2);
-            // a scale of 0 (its codes are 0 too) as one that changes nothing; NaN stays
+            // a scale of 0: codes of 0, weight still in l; NaN stays
             const float lvl = vs <= 0x1p-100f ? -100.f : __log2f(vs);
             const float inv = ex2_approx(-lvl);
-            const float ksl = ks <= 1e-30f ? 1e-30f : ks;
 
             ok = __all_sync(0xffffffffu, mbar_wait_sleep(&s_full[bb], uint32_t(j / NS) & 1, abort));
             if (!ok) break;
@@ -442,12 +443,15 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
 #pragma unroll
                 for (int i = 0; i < BN; ++i) s[i] = (s[i] - bias) * ce;
             }
-            // exponent of value s in page pg: s * c[pg] + a[pg]
+            // exponent of value s in page pg: s * c[pg] + a[pg].  c stays above 0, so that
+            // a masked value (s = -inf) keeps its exponent where the keys or the row are 0
+            // or tiny: |s| < 2^20, so the other exponents do not notice
             float c[Cfg::kPages], a[Cfg::kPages];
 #pragma unroll
             for (int pg = 0; pg < Cfg::kPages; ++pg) {
-                const float k1 = __shfl_sync(0xffffffffu, ksl, pg), v1 = __shfl_sync(0xffffffffu, lvl, pg);
-                c[pg] = positive ? ce * k1 : k1;
+                const float k1 = __shfl_sync(0xffffffffu, ks, pg), v1 = __shfl_sync(0xffffffffu, lvl, pg);
+                const float c1 = positive ? ce * k1 : k1;
+                c[pg] = c1 < 0x1p-126f ? 0x1p-126f : c1;  // NaN stays
                 a[pg] = positive ? fmaf(-bias, c[pg], v1) : v1;
             }
             if (!(n0 >= lo && n0 + BN <= lim) && n0 + BN > sink) {

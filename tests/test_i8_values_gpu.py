@@ -1,0 +1,72 @@
+"""Values at the ends of what the 8-bit attention calls take: queries from the
+smallest bf16 to large ones, blocks of zero keys.  Against the definition in 64
+bits, with the bounds of the arithmetic that the kernels use."""
+import pytest
+import torch
+
+from tests import serving_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+# |out - definition| <= 2^-8 |out| for its rounding to bf16, plus this part of the
+# weighted mean of |V|: weights as f16 (2^-11 each) against a sum of unrounded ones.
+MULTI = 2.0 ** -11
+
+
+@pytest.fixture(scope="module")
+def pa():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from paged_kv_attention_36_b200 import binding
+    binding.pa_device_errors(clear=True)
+    return binding
+
+
+def _multi(pa, q, cache, n, scale, window=ref.ALL, sinks=0):
+    """The last q.shape[0] tokens of one sequence of n tokens."""
+    out = torch.full_like(q, float("nan")).cuda()
+    k, v, ks, vs, bt = [t.cuda() for t in cache]
+    pa.pa_prefill_i8(q.cuda(), torch.tensor([0, q.shape[0]], dtype=torch.int32).cuda(), q.shape[0], k, v, ks, vs, bt,
+                     torch.tensor([n], dtype=torch.int32).cuda(), scale, out, window=window, sinks=sinks)
+    assert pa.pa_device_errors(clear=True) == 0
+    return out
+
+
+def _want(q, cache, n, scale, window=ref.ALL, sinks=0):
+    k, v, ks, vs, bt = cache
+    return ref.attend(q, *ref.values_i8(k, v, ks, vs, bt[0], n), scale, window, sinks)
+
+
+TINY = 2.0 ** -133  # bf16's smallest
+
+
+@pytest.mark.parametrize("n,rows", [(300, 40), (4000, 3)])  # a tile a CTA, a tile a cluster
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [TINY, 2.0 ** -128, 2.0 ** -126, 1e-30, 1e-6, 1e5, 1e30])
+def test_prefill_i8_query_sizes(pa, size, D, n, rows):
+    g = torch.Generator().manual_seed(D)
+    cache = ref.i8_batch(g, [n], 2, D)
+    q = torch.randn((rows, 8, D), generator=g)
+    if size < 1e-37:  # a few steps of the smallest value, zeros among them
+        q = q.clamp(-3, 3).round()
+    q = (q.double() * size).bfloat16()
+    assert (q[0] != 0).any()
+    scale = min(D ** -0.5 / size, 1e38)  # logits of size 1, or none to speak of
+    want, mean_abs = _want(q, cache, n, scale)
+    ref.assert_attention(_multi(pa, q, cache, n, scale), want, mean_abs, MULTI)
+
+
+@pytest.mark.parametrize("n,rows", [(300, 40), (4000, 3)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("size", [TINY, 2.0 ** -127, 1e-30, 1e-15])
+def test_prefill_i8_tiny_queries_and_zero_keys(pa, size, D, n, rows):
+    # blocks of zero keys have a scale of 0; the row's own page and the window's first are seen in part
+    g = torch.Generator().manual_seed(D + 1)
+    k, v, ks, vs, bt = ref.i8_batch(g, [n], 2, D)
+    for page in range(0, (n + 15) // 16, 2):
+        k[int(bt[0, page])] = 0
+        ks[int(bt[0, page])] = 0.0
+    q = (torch.randn((rows, 8, D), generator=g).clamp(-3, 3).round().double() * size).bfloat16()
+    for window in (ref.ALL, 165):
+        want, mean_abs = _want(q, (k, v, ks, vs, bt), n, 0.125, window)
+        ref.assert_attention(_multi(pa, q, (k, v, ks, vs, bt), n, 0.125, window), want, mean_abs, MULTI)
