@@ -8,17 +8,16 @@
 //   * Four converter warps take the place of the TMA producer.  They read the
 //     tiles' codes into registers one block ahead (a tile is contiguous: each
 //     thread has the same 16 bytes of every page), and write f16 operands
-//     into the swizzled ring.  A code b becomes an f16 by its bytes alone:
-//     0x6400 | (b ^ 0x80) is 1152 + b.  V takes the 1152 back value by value
-//     (exact; its sums run over the whole context).  K keeps it: a row's
-//     logits are then all 1152 sum(q) times too large before the scales,
-//     which the softmax's fma takes away with the page's K scale.
+//     into the swizzled ring.  A code b becomes an f16 by its bytes,
+//     0x6400 | (b ^ 0x80) is 1152 + b, and an exact subtraction.  (Keys that
+//     kept the 1152 would save the subtraction, but their logits would be
+//     differences of sums as large as 1152 sum(q).)
 //   * V stays transposed: its tile rows are head_dim, so a block is the
 //     K-major B operand [D][64 tokens] of P V.
 //   * Queries are scaled by a power of two to below 4 in f16, which loses
 //     nothing bf16 holds down to 2^-14 of the row's largest value.
 //   * Scales cost no work per value: with c = scale * log2(e) * k_scale of
-//     the page and v = log2(v_scale), P = 2^(s c + (v - m - bias c)) is the
+//     the page and v = log2(v_scale), P = 2^(s c + (v - m)) is the
 //     weight times v_scale, so P V needs no scale, and l adds the page's sum
 //     of P times 1 / v_scale.  m is the largest exponent less kLift, raised
 //     when one passes it by 15: P lies in [0, 2^15], and f16's smallest step
@@ -102,7 +101,6 @@ struct PrefillI8Params {
 };
 
 // 16 codes as f16 pairs in order: words 0-3 the first 8 values, 4-7 the next.
-template <bool EXACT>
 __device__ __forceinline__ void codes_to_f16(const uint4& r, uint32_t (&o)[8]) {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -110,13 +108,11 @@ __device__ __forceinline__ void codes_to_f16(const uint4& r, uint32_t (&o)[8]) {
         const uint32_t x = w[i] ^ 0x80808080u;
         o[2 * i] = __byte_perm(x, 0x64646464u, 0x4140);
         o[2 * i + 1] = __byte_perm(x, 0x64646464u, 0x4342);
-        if constexpr (EXACT) {
-            const __half2 b = __floats2half2_rn(1152.f, 1152.f);
+        const __half2 b = __floats2half2_rn(1152.f, 1152.f);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&o[2 * i + k]), b);
-                o[2 * i + k] = *reinterpret_cast<const uint32_t*>(&v);
-            }
+        for (int k = 0; k < 2; ++k) {
+            const __half2 v = __hsub2(*reinterpret_cast<const __half2*>(&o[2 * i + k]), b);
+            o[2 * i + k] = *reinterpret_cast<const uint32_t*>(&v);
         }
     }
 }
@@ -322,7 +318,7 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
                     // theirs in the other order, into the banks the first's leave
                     const bool f = D == 128 && cc >= 4;
                     uint32_t o[8];
-                    codes_to_f16<false>(f ? make_uint4(kr[i].z, kr[i].w, kr[i].x, kr[i].y) : kr[i], o);
+                    codes_to_f16(f ? make_uint4(kr[i].z, kr[i].w, kr[i].x, kr[i].y) : kr[i], o);
                     const int row = page_in_block(i) * 16 + t_in;  // row % 8 = t_in % 8
                     uint8_t* dst = kb + (cc >> 2) * Cfg::kPanelK + row * 128;
                     const int ch = ((cc & 3) * 2) ^ (t_in & 7) ^ (f ? 1 : 0);
@@ -348,7 +344,7 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
                 for (int i = 0; i < NP; ++i) {
                     // stored byte order: words hold tokens 2c, 2c+1, 2c+8, 2c+9
                     uint32_t o[8];
-                    codes_to_f16<true>(vr[i], o);
+                    codes_to_f16(vr[i], o);
                     uint8_t* dst = vb + d_in * 128;
                     const int ch = page_in_block(i) * 2;
                     *reinterpret_cast<uint4*>(dst + ((ch ^ (d_in & 7)) << 4)) = make_uint4(o[0], o[2], o[4], o[6]);
@@ -376,12 +372,12 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
         const int sink = sinks < lim ? sinks : lim;
 
         // ---- Q row: a power of two times it, as f16, in shared memory ----
-        float ce, bias;  // logits = (s - bias) * ce * k_scale
+        float ce;  // logits = s * ce * k_scale
         {
             uint4 qv[D / 8];
             const uint4* src =
                 reinterpret_cast<const uint4*>(p.q + ((int64_t(q0) + r / G) * p.Hq + g * G + r % G) * (D * 2));
-            float top = 0.f, sum = 0.f;
+            float top = 0.f;
 #pragma unroll
             for (int ch = 0; ch < D / 8; ++ch) {
                 qv[ch] = valid ? __ldg(src + ch) : make_uint4(0u, 0u, 0u, 0u);
@@ -403,8 +399,6 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
                 for (int i = 0; i < 4; ++i) {
                     const float2 f = bf16x2_to_float2(w[i]);
                     w[i] = float2_to_f16x2(f.x * down, f.y * down);
-                    const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                    sum += h.x + h.y;
                 }
                 *reinterpret_cast<uint4*>(qs + (ch >> 3) * Cfg::kPanelQ + row * 128 + (((ch & 7) ^ (row & 7)) << 4)) =
                     make_uint4(w[0], w[1], w[2], w[3]);
@@ -412,7 +406,6 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
             fence_proxy_async_smem();
             mbar_arrive(q_full);
             ce = p.qscale * __uint_as_float(uint32_t(127 + e) << 23);
-            bias = 1152.f * sum;
         }
         const bool positive = ce > 0.f;
 
@@ -441,18 +434,18 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
             tmem_ld2x32(tmem + lanes + bb * BN, s);
             if (!positive) {
 #pragma unroll
-                for (int i = 0; i < BN; ++i) s[i] = (s[i] - bias) * ce;
+                for (int i = 0; i < BN; ++i) s[i] *= ce;
             }
             // exponent of value s in page pg: s * c[pg] + a[pg].  c stays above 0, so that
             // a masked value (s = -inf) keeps its exponent where the keys or the row are 0
-            // or tiny: |s| < 2^20, so the other exponents do not notice
+            // or tiny: |s| < 2^16, so the other exponents do not notice
             float c[Cfg::kPages], a[Cfg::kPages];
 #pragma unroll
             for (int pg = 0; pg < Cfg::kPages; ++pg) {
                 const float k1 = __shfl_sync(0xffffffffu, ks, pg), v1 = __shfl_sync(0xffffffffu, lvl, pg);
                 const float c1 = positive ? ce * k1 : k1;
                 c[pg] = c1 < 0x1p-126f ? 0x1p-126f : c1;  // NaN stays
-                a[pg] = positive ? fmaf(-bias, c[pg], v1) : v1;
+                a[pg] = v1;
             }
             if (!(n0 >= lo && n0 + BN <= lim) && n0 + BN > sink) {
 #pragma unroll

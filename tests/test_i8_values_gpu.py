@@ -1,5 +1,5 @@
 """Values at the ends of what the 8-bit attention calls take: queries from the
-smallest bf16 to large ones, blocks of zero keys.  Against the definition in 64
+smallest bf16 to large ones and far from zero mean, blocks of zero keys.  Against the definition in 64
 bits, with the bounds of the arithmetic that the kernels use."""
 import pytest
 import torch
@@ -70,3 +70,28 @@ def test_prefill_i8_tiny_queries_and_zero_keys(pa, size, D, n, rows):
     for window in (ref.ALL, 165):
         want, mean_abs = _want(q, (k, v, ks, vs, bt), n, 0.125, window)
         ref.assert_attention(_multi(pa, q, (k, v, ks, vs, bt), n, 0.125, window), want, mean_abs, MULTI)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_i8_queries_far_from_zero_mean(pa, D):
+    # every row sees two tokens with values +1 and -1, so out = tanh of half the logits' difference.
+    # Queries are 256 but for 8 columns of 258, keys sum to zero over the columns: a logit is the small
+    # difference of large products.  Column pairs cancel but for 2 code, so a partial sum of whole pairs
+    # is below 2^11, and one within 16 columns below 2^18: D / 16 roundings of 2^-24 of that are at most
+    # 0.13 of a logit's unit (q times code), of which 413 make a logit of 1.  The difference of two logits
+    # is off by 2^-10.6 at most, out by half of that: inside the 2^-11 + 2^-12 of the check.
+    g = torch.Generator().manual_seed(D)
+    n = 90
+    k, v, ks, vs, bt = ref.i8_batch(g, [n], 2, D)
+    half = torch.randint(-127, 128, (k.shape[0], 2, 16, D // 2), generator=g).to(torch.int8)
+    k = torch.stack([half, -half], dim=-1).flatten(-2).contiguous()
+    ks.fill_(1.0)
+    by_byte = torch.empty(16, dtype=torch.int8)
+    by_byte[torch.tensor(ref.V_BYTES)] = torch.tensor([127 - 254 * (t % 2) for t in range(16)], dtype=torch.int8)
+    v = by_byte.expand(v.shape).contiguous()
+    vs.fill_(1 / 127)
+    q = torch.full((n, 8, D), 256.0)
+    q[..., : 16: 2] = 258.0
+    q = q.bfloat16()
+    want, mean_abs = _want(q, (k, v, ks, vs, bt), n, 1 / 413, 2)
+    ref.assert_attention(_multi(pa, q, (k, v, ks, vs, bt), n, 1 / 413, 2), want, mean_abs, MULTI)
