@@ -371,7 +371,9 @@ PA_API pa_status pa_prefill(const void* q, const int32_t* cu_q_lens, int32_t max
  * else PA_ERR_SHAPE.  Only pages that hold a token some query of the call
  * sees are read, so block-table entries of other pages may hold anything (a
  * block that slid out of the window can be given away), and so may cached
- * rows that no query sees.
+ * rows that no query sees.  A cached value that is not finite makes the
+ * outputs of the queries that see it not finite (a V value in its column) and
+ * leaves the other queries' alone.
  *
  * pa_decode_window: pa_decode with the window (position p = L_b - 1); the
  * workspace as for pa_decode.  pa_prefill_window: pa_prefill with the

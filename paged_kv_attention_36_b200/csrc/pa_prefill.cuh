@@ -35,6 +35,7 @@ struct PrefillParams {
     int32_t tiles_per_seq;          // ceil(max_q_len * G / (16 * NW))
     float qscale;                   // scale * log2(e)
     int32_t window, sinks;          // WINDOW: tokens t > position - window or t < sinks count
+    const uint8_t* v_cache;         // WINDOW: [NB][Hkv][16][D] bf16, for values that are not finite
 };
 
 template <int D, int G, int NW, int RS>

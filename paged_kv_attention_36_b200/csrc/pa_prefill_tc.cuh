@@ -158,6 +158,56 @@ struct SplitRows {
     }
 };
 
+// bf16 pairs: all ones in the halves that are NaN or infinite.
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) { return __vcmpgeu2(w & 0x7fff7fffu, 0x7f807f80u); }
+
+// Values that are not finite in a windowed tile.  In a matrix product a weight of
+// 0 times such a value is NaN, so rows that do not see a key would have it too.
+// Where a tile's sums end so, a second pass takes these values out of the blocks
+// that some rows see and others do not (in shared memory), and adds them to the
+// staged rows (O or the output) that see them: those columns are then NaN or
+// infinite, whatever the weight.  (Finding out takes 0.4-0.9 us of a call; looking
+// through such blocks in every tile took 53 in place of 43 us on 13 ragged chunks
+// of up to 700 tokens with a window of 333.)
+struct WindowRow {
+    const uint8_t* v_cache;
+    const int32_t* bt;             // of the CTA's list
+    int32_t NB, Hkv, g;
+    int32_t ns, skip, pages;       // the list
+    int32_t sink, lo, lim;         // this row sees list keys [0, sink) and [lo, lim)
+    int32_t sink_all, lo_last, lim_first;  // every row sees [0, sink_all) and [lo_last, lim_first)
+};
+template <int D, int BN, class T>
+__device__ __forceinline__ void add_nonfinite(const WindowRow& w, T* row) {
+    for (int n0 = 0; n0 < w.pages * 16; n0 += BN) {
+        if (n0 + BN <= w.sink_all || (n0 >= w.lo_last && n0 + BN <= w.lim_first)) continue;  // multiplied as it is
+        for (int n = n0; n < n0 + BN && n < w.pages * 16; ++n) {
+            if (!(n < w.sink || (n >= w.lo && n < w.lim))) continue;
+            const int pg = n / 16;
+            int32_t blk = w.bt[pg >= w.ns ? pg + w.skip : pg];
+            if (blk < 0 || blk >= w.NB) blk = 0;
+            const uint4* v = reinterpret_cast<const uint4*>(
+                w.v_cache + ((int64_t(blk) * w.Hkv + w.g) * 16 + n % 16) * (D * 2));
+            for (int ch = 0; ch < D / 8; ++ch) {
+                const uint4 x = v[ch];
+                const uint32_t word[4] = {x.x, x.y, x.z, x.w};
+                for (int i = 0; i < 8; ++i)
+                    if (nonfinite2(word[i / 2]) >> (16 * (i % 2)) & 1) {
+                        const float bad = __uint_as_float(i % 2 ? word[i / 2] & 0xffff0000u : word[i / 2] << 16);
+                        row[8 * ch + i] = T(float(row[8 * ch + i]) + bad);
+                    }
+            }
+        }
+    }
+}
+
+// Whether the int at `flag` (shared memory) is set in one of the cluster's first n CTAs.
+__device__ __forceinline__ bool any_rank(const int* flag, int n) {
+    bool any = false;
+    for (int i = 0; i < n; ++i) any |= ld_cluster_s32(cluster_addr(smem_u32(flag), i)) != 0;
+    return any;
+}
+
 template <int D, int BN, int KS, int NS>
 struct TcPrefillCfg {
     static constexpr int kBM = 128;                 // query rows of a CTA
@@ -172,7 +222,10 @@ struct TcPrefillCfg {
     static constexpr int kStageOff = kQBytes;
     static constexpr int kBarOff = kStageOff + KS * kStage;
     static constexpr int kNumBars = 1 + 4 * KS + 2 * NS + 1;
-    static constexpr int kSmemBytes = kBarOff + kNumBars * 8 + 16 + 1024;  // + TMEM slot, alignment slack
+    static constexpr int kTmemSlotOff = kBarOff + kNumBars * 8;
+    static constexpr int kBars2Off = kTmemSlotOff + 16;  // barriers of a windowed tile's second pass
+    static constexpr int kSmemBytes = kBars2Off + 1024;  // + alignment slack
+    static constexpr int kWindowSmemBytes = kSmemBytes + kNumBars * 8;
     static constexpr int kThreads = 6 * 32;
     static constexpr int kColsUsed = NS * BN + D;  // S buffers, then O
     static constexpr int kTmemCols = kColsUsed <= 32 ? 32 : kColsUsed <= 64 ? 64 : kColsUsed <= 128 ? 128
@@ -195,8 +248,11 @@ struct TcPrefillCfg {
 // (blocks of 64 keys at the window's edges are multiplied whole).
 // SPLIT (WINDOW): a cluster of CTAs on each tile (KeySplit).  A kernel of its own:
 // the same code in the unsplit one costs it registers (127 against 122 us above).
-template <bool PREFIX, int D, int G, int BN, int KS, int NS, bool WINDOW = false, bool SPLIT = false, class Params>
-__device__ __forceinline__ void tc_attention_tile(const Params& p) {
+// SECOND (WINDOW): the pass after one that returned true, in every CTA of the tile
+// (WindowRow); it has the first one's tensor memory and barriers of its own.
+template <bool PREFIX, int D, int G, int BN, int KS, int NS, bool WINDOW = false, bool SPLIT = false,
+          bool SECOND = false, class Params>
+__device__ __forceinline__ bool tc_attention_tile(const Params& p) {
     using Cfg = TcPrefillCfg<D, BN, KS, NS>;
     static_assert(Cfg::kBM % G == 0, "a tile holds whole tokens (members)");
     constexpr bool kKOnV = KS >= 4;  // release K ring slots with the V ones (deep rings)
@@ -204,7 +260,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t* qs = smem;
     uint8_t* stages = smem + Cfg::kStageOff;
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + Cfg::kBarOff);
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + (SECOND ? Cfg::kBars2Off : Cfg::kBarOff));
     uint64_t* k_full = q_full + 1;  // K and V halves of a stage fill and drain separately
     uint64_t* v_full = k_full + KS;
     uint64_t* k_empty = v_full + KS;
@@ -212,8 +268,9 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     uint64_t* s_full = v_empty + KS;
     uint64_t* p_full = s_full + NS;
     uint64_t* drain = p_full + NS;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kTmemSlotOff);
     __shared__ int s_abort, s_ranks;  // s_ranks (SPLIT): CTAs that share the tile
+    __shared__ int s_nonfinite;       // a second pass is needed; in it, that values were taken out of blocks
     volatile int* abort = &s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int g = blockIdx.y;
@@ -234,7 +291,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
             tile = mine.tile;
             g = mine.g;
         }
-        if (b >= p.B) return;
+        if (b >= p.B) return false;
         const bool report = tile == 0 && g == 0 && threadIdx.x == 0;
         L = __ldg(p.context_lens + b);
         const int64_t cap = int64_t(p.M) * 16;
@@ -250,7 +307,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         }
         nrows = q_len * G;
         row0 = tile * Cfg::kBM;
-        if (row0 >= nrows) return;  // whole CTA, before any barrier or TMEM use
+        if (row0 >= nrows) return false;  // whole CTA, before any barrier or TMEM use
         first_pos = L - q_len;      // position of query token 0
         const int last_row = (row0 + Cfg::kBM < nrows ? row0 + Cfg::kBM : nrows) - 1;
         nkeys = first_pos + last_row / G + 1;  // tokens 0 .. nkeys-1 are visible to some row
@@ -267,7 +324,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     } else {
         const int gi = int(blockIdx.x) / p.tiles_per_group;
         const int tile = int(blockIdx.x) - gi * p.tiles_per_group;
-        if (gi >= p.num_groups) return;
+        if (gi >= p.num_groups) return false;
         first = __ldg(p.group_offsets + gi);
         int last = __ldg(p.group_offsets + gi + 1);
         P = __ldg(p.group_prefix_pages + gi);
@@ -281,11 +338,11 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         }
         nrows = (last - first) * G;
         row0 = tile * Cfg::kBM;
-        if (P <= 0 || row0 >= nrows) return;
+        if (P <= 0 || row0 >= nrows) return false;
         const int per = prefix_split_pages(P, gridDim.z);
         pg0 = int(blockIdx.z) * per;
         const int pg1 = pg0 + per < P ? pg0 + per : P;
-        if (pg0 >= pg1) return;
+        if (pg0 >= pg1) return false;
         nkeys = (pg1 - pg0) * 16;  // shared pages are whole
         bt = p.block_tables + int64_t(first) * p.M + pg0;  // the group leader's table
     }
@@ -295,7 +352,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     if constexpr (SPLIT) {
         const KeySplit split(nblk);
         const int rank = int(cluster_rank());
-        if (rank >= split.ranks) return;  // before any barrier or TMEM use
+        if (rank >= split.ranks) return false;  // before any barrier or TMEM use
         if (threadIdx.x == 0) s_ranks = split.ranks;
         // the list from this rank's first block on: pages, keys and sinks count from there
         const int first_pg = rank * split.per * Cfg::kPages;
@@ -339,9 +396,10 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         }
         mbar_init(drain, 1);
         s_abort = 0;
+        if constexpr (WINDOW) s_nonfinite = 0;
         fence_mbar_init();
     }
-    if (warp == 1) {
+    if (!SECOND && warp == 1) {
         tmem_alloc(tmem_slot, Cfg::kTmemCols);
         tmem_relinquish();
     }
@@ -351,6 +409,7 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     const uint32_t tmem = *tmem_slot;
     const uint32_t t_o = tmem + NS * BN;  // O columns; S buffer i at tmem + i*BN
 
+    bool again_ranks = false;  // SPLIT: some rank's sums do not stand
     if (warp == 0) {
         // ======================= producer warp =======================
         if (lane == 0) {
@@ -481,9 +540,15 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         const int pos1 = first_pos + r / G + 1;  // the row's position + 1
         const int lim = PREFIX ? nkeys : WINDOW ? (valid ? pos1 - shift : nkeys) : (valid ? pos1 : 1);
         int lo = 0, sink = 0;
+        int lim_first = 0, lo_last = 0, sink_all = 0;  // every row sees keys [0, sink_all) and [lo_last, lim_first)
         if constexpr (WINDOW) {
             lo = window_first(lim - 1 + shift, p.window) - shift;
             sink = sinks < lim ? sinks : lim;
+        }
+        if constexpr (SECOND) {
+            lim_first = first_pos + row0 / G + 1 - shift;
+            lo_last = window_first(nkeys - 1 + shift, p.window) - shift;
+            sink_all = sinks < lim_first ? sinks : lim_first;
         }
         const int64_t qrow = int64_t(PREFIX ? first : q0) + r / G;
 
@@ -591,7 +656,28 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
                 l += (a0 + a1) + (b0 + b1);
             }
             tmem_st_wait();
-            if constexpr (WINDOW) {
+            if constexpr (SECOND) {
+                // a block that some row does not see whole (and V rows that no row does)
+                if (!(n0 + BN <= sink_all || (n0 >= lo_last && n0 + BN <= lim_first))) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_sleep(&v_full[j % KS], uint32_t(j / KS) & 1, abort));
+                    if (!ok) break;
+                    uint8_t* vz = stages + (j % KS) * Cfg::kStage + Cfg::kKBytes;
+#pragma unroll
+                    for (int i = gt; i < BN * 8 * Cfg::kPanels; i += 128) {
+                        const int pc = i / (BN * 8), rr = i - pc * (BN * 8), n = n0 + (rr >> 3);
+                        uint4* at = reinterpret_cast<uint4*>(vz + pc * Cfg::kPanelKV + rr * 16);
+                        const uint4 v = *at;
+                        const uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                                      __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                        if (n < pages * 16 && nonfinite2(top)) {
+                            *at = make_uint4(v.x & ~nonfinite2(v.x), v.y & ~nonfinite2(v.y), v.z & ~nonfinite2(v.z),
+                                             v.w & ~nonfinite2(v.w));
+                            fence_proxy_async_smem();
+                            if (n < nkeys && (n < sinks || n >= f0)) s_nonfinite = 1;  // some row sees it
+                        }
+                    }
+                }
+            } else if constexpr (WINDOW) {
                 // V rows of the list that no row of the tile sees: between the
                 // sinks and the first window, and past the context
                 const int gap = sinks > n0 ? sinks : n0, gap_end = f0 < n0 + BN ? f0 : n0 + BN;
@@ -633,6 +719,15 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
         if (ok)
             ok = __all_sync(0xffffffffu,
                             mbar_wait_sleep(&v_empty[(nblk - 1) % KS], uint32_t((nblk - 1) / KS) & 1, abort));
+        bool nonfinite = false;
+        if constexpr (SECOND) {
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // every warp's blocks are done
+            nonfinite = s_nonfinite != 0;
+        }
+        float probe[4] = {0.f, 0.f, 0.f, 0.f};  // WINDOW, first pass: NaN once a sum of the row is not finite
+        auto window_row = [&](const auto& a) {
+            return WindowRow{a.v_cache, bt, a.NB, a.Hkv, g, ns, skip, pages, sink, lo, lim, sink_all, lo_last, lim_first};
+        };
         constexpr int kRowBytes = D * (PREFIX ? 4 : 2);
         constexpr int kRowStride = kRowBytes + 16;
         static_assert(Cfg::kBM * kRowStride <= Cfg::kBarOff, "output staging fits in the Q and ring space");
@@ -644,9 +739,17 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
                 for (int k = 0; k < D / 32; ++k) {
                     float o[32];
                     tmem_ld32(t_o + lanes + 32 * k, o);
+                    if constexpr (!SECOND) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) probe[i & 3] = fmaf(o[i], 0.f, probe[i & 3]);
+                    }
                     SplitRows<D>::store(smem, row, o, 32 * k);
                 }
                 *reinterpret_cast<float2*>(smem + SplitRows<D>::kMl + row * 8) = make_float2(m, l);
+                if constexpr (SECOND) {
+                    if (nonfinite)
+                        add_nonfinite<D, BN>(window_row(p), reinterpret_cast<float*>(smem + row * SplitRows<D>::kStride));
+                }
             }
         } else if (ok) {
             tc_fence_after();
@@ -656,6 +759,10 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
             for (int k = 0; k < D / 64; ++k) {
                 float o[64];
                 tmem_ld64(t_o + lanes + 64 * k, o);
+                if constexpr (WINDOW && !SECOND) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) probe[i & 3] = fmaf(o[i], 0.f, probe[i & 3]);
+                }
                 if constexpr (!PREFIX) {
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
@@ -671,25 +778,41 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
                             make_float4(o[4 * q] * inv, o[4 * q + 1] * inv, o[4 * q + 2] * inv, o[4 * q + 3] * inv);
                 }
             }
+            if constexpr (SECOND) {
+                if (nonfinite) add_nonfinite<D, BN>(window_row(p), reinterpret_cast<__nv_bfloat16*>(mine));
+            }
             if constexpr (PREFIX) {
                 // (max logit in base 2, exp-sum) of the row's partial
                 if (valid) p.prefix_ml[(int64_t(blockIdx.z) * p.B + qrow) * p.Hq + g * G + r % G] = make_float2(m, l);
             }
         }
-        bool whole = true;  // this CTA holds the tile's sums
+        bool whole = true;  // this CTA holds the tile's sums, and they stand
+        if constexpr (WINDOW && !SECOND) {
+            // the rows are staged; one whose keys are not finite (l) stays as it is
+            const float any = (probe[0] + probe[1]) + (probe[2] + probe[3]);
+            const bool again = bar_any_128(valid && any != any && l < INFINITY);
+            if (again) {
+                s_nonfinite = 1;
+                fence_proxy_async_smem();  // the staged rows, before the ring is filled again
+            }
+            whole = !again;
+        } else {
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // the 4 softmax warps: rows staged
+        }
         if constexpr (SPLIT) {
-            whole = s_ranks == 1;
-            if (!whole) {
+            if (s_ranks > 1) {
+                whole = false;
                 __syncwarp();
                 cluster_sync();  // every rank's rows are staged
-                SplitRows<D>::join(smem, s_ranks, nrows - row0 < Cfg::kBM ? nrows - row0 : Cfg::kBM,
-                                   (warp - 2) * 32 + lane, [&](int rr) {
-                                       const int rg = row0 + rr;
-                                       return p.out + ((int64_t(q0) + rg / G) * p.Hq + g * G + rg % G) * D;
-                                   });
+                if (!SECOND) again_ranks = any_rank(&s_nonfinite, s_ranks);
+                if (!again_ranks)
+                    SplitRows<D>::join(smem, s_ranks, nrows - row0 < Cfg::kBM ? nrows - row0 : Cfg::kBM,
+                                       (warp - 2) * 32 + lane, [&](int rr) {
+                                           const int rg = row0 + rr;
+                                           return p.out + ((int64_t(q0) + rg / G) * p.Hq + g * G + rg % G) * D;
+                                       });
             }
         }
-        if (whole) asm volatile("bar.sync 1, 128;" ::: "memory");  // the 4 softmax warps: rows staged
         if (!*abort && whole) {
             constexpr int kChunks = kRowBytes / 16;       // 16-byte chunks per row
             constexpr int kRowsPerPass = 32 / kChunks;    // rows per warp instruction
@@ -731,7 +854,10 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     if constexpr (SPLIT) {
         if (s_ranks > 1) {
             __syncwarp();
-            if (warp < 2) cluster_sync();
+            if (warp < 2) {
+                cluster_sync();
+                if (!SECOND) again_ranks = any_rank(&s_nonfinite, s_ranks);
+            }
             cluster_sync();  // every rank's rows are read
         }
     }
@@ -739,10 +865,22 @@ __device__ __forceinline__ void tc_attention_tile(const Params& p) {
     // ---- release TMEM once every warp's tcgen05 work has finished ----
     tc_fence_before();
     __syncthreads();
+    if constexpr (WINDOW && !SECOND) {
+        if (SPLIT && s_ranks > 1 ? again_ranks : s_nonfinite != 0) {
+            tc_fence_after();
+            return true;
+        }
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, Cfg::kTmemCols);
     }
+    return false;
+}
+
+template <int D, int G, int BN, int KS, int NS, bool SPLIT>
+__device__ __noinline__ void window_second_pass(const PrefillParams& p) {
+    tc_attention_tile<false, D, G, BN, KS, NS, true, SPLIT, true>(p);
 }
 
 template <int D, int G, int BN, int KS, int CPS, int NS, bool WINDOW = false, bool SPLIT = false>
@@ -751,7 +889,10 @@ __global__ void __launch_bounds__(6 * 32, CPS) prefill_tc_kernel(const __grid_co
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         asm volatile("griddepcontrol.wait;" ::: "memory");
     }
-    tc_attention_tile<false, D, G, BN, KS, NS, WINDOW, SPLIT>(p);
+    const bool again = tc_attention_tile<false, D, G, BN, KS, NS, WINDOW, SPLIT>(p);
+    if constexpr (WINDOW) {
+        if (again) window_second_pass<D, G, BN, KS, NS, SPLIT>(p);
+    }
 }
 
 // The shared-prefix (cascade) pass on tcgen05: grid (group x row tile, kv

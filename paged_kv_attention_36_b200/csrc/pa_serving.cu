@@ -77,6 +77,7 @@ void fill_prefill(const Call& c, pa::PrefillParams& p) {
     p.qscale = c.scale * kLog2e;
     p.window = c.window;
     p.sinks = c.sinks;
+    p.v_cache = static_cast<const uint8_t*>(c.v_cache);
 }
 
 // fn<D, G>() for the head_dim and GQA group of a call that supported() let through.
@@ -252,11 +253,11 @@ struct PrefillWindow {
         using S = TcShape<D, 64>;
         auto kern = pa::prefill_tc_kernel<D, G, 64, S::KS, S::CPS, S::NS, true, SPLIT>;
         static unsigned attr_done[kMaxDevices];
-        if (!set_smem_once(kern, SPLIT ? kAloneSmem : S::Cfg::kSmemBytes, attr_done, SPLIT)) return PA_ERR_CUDA;
-        static_assert(S::Cfg::kSmemBytes <= kAloneSmem);
+        if (!set_smem_once(kern, SPLIT ? kAloneSmem : S::Cfg::kWindowSmemBytes, attr_done, SPLIT)) return PA_ERR_CUDA;
+        static_assert(S::Cfg::kWindowSmemBytes <= kAloneSmem);
         static std::atomic<int> held[kMaxDevices * 8];
         const bool alone = SPLIT && fits_alone(kern, S::Cfg::kThreads, tiles, cluster, held);
-        const int smem = alone ? kAloneSmem : S::Cfg::kSmemBytes;
+        const int smem = alone ? kAloneSmem : S::Cfg::kWindowSmemBytes;
         return launch_dependent(kern, dim3(tiles * cluster), S::Cfg::kThreads, smem, stream, p, cluster);
     }
     template <int D, int G>
