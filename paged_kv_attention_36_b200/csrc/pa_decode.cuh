@@ -472,8 +472,8 @@ struct MmaMath {
         for (int ks = 0; ks < KS; ++ks) {
             if (h < G) {
                 const uint32_t* row = reinterpret_cast<const uint32_t*>(gq + h * D * 2);
-                qb[ks][0] = __ldg(row + (16 * ks + kk) / 2);
-                qb[ks][1] = __ldg(row + (16 * ks + kk + 8) / 2);
+                qb[ks][0] = __ldca(row + (16 * ks + kk) / 2);
+                qb[ks][1] = __ldca(row + (16 * ks + kk + 8) / 2);
             } else {
                 qb[ks][0] = qb[ks][1] = 0u;
             }
@@ -961,7 +961,7 @@ __device__ __forceinline__ long long block_incl_scan(long long v, long long* red
 
 template <int BS>
 __device__ __forceinline__ int32_t clamp_len(const DecodeParams& p, int b, bool report) {
-    int32_t L = __ldg(p.context_lens + b);
+    int32_t L = __ldca(p.context_lens + b);
     const int64_t cap = int64_t(p.M) * BS;
     if (L < 0 || L > cap) {
         if (report) raise_error(PA_DEVERR_CONTEXT);

@@ -133,7 +133,7 @@ struct I8Math : MmaMath<D, G, 16> {
         for (int j = 0; j < D / 32; ++j)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                w[j][i] = h < G ? __ldg(reinterpret_cast<const uint2*>(gq + (h * D + 32 * j + 16 * i + 4 * c) * 2))
+                w[j][i] = h < G ? __ldca(reinterpret_cast<const uint2*>(gq + (h * D + 32 * j + 16 * i + 4 * c) * 2))
                                 : make_uint2(0u, 0u);
                 const float2 x = bf16x2_to_float2(w[j][i].x), y = bf16x2_to_float2(w[j][i].y);
                 top = fmaxf(fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(y.x), fabsf(y.y)));
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
                     ++n.b;
                     n.L = checked(L_next);
                     while (n.L == 0) n.L = clamp_len<16>(p, ++n.b, false);
-                    if (n.b + 1 < p.B) L_next = __ldg(p.context_lens + n.b + 1);
+                    if (n.b + 1 < p.B) L_next = __ldca(p.context_lens + n.b + 1);
                 }
                 cut(n, pages_of(n).np);
             } while (n.npg == 0);
@@ -704,7 +704,7 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
         auto block_of = [&](const Seg& g, int c0) -> int32_t {
             const int x = c0 + lane;
             if (lane >= C || x >= g.npg << sh.SPL_LOG) return 0;
-            return __ldg(p.block_tables + int64_t(g.b) * p.M + pages_of(g).page(g.j + (x >> sh.SPL_LOG)));
+            return __ldca(p.block_tables + int64_t(g.b) * p.M + pages_of(g).page(g.j + (x >> sh.SPL_LOG)));
         };
 
         Seg seg;
@@ -714,11 +714,11 @@ __global__ void __launch_bounds__(kWideThreads, 1) decode_wide_kernel(const __gr
         seg.hg = p_start - misc->pre0 < unit0 ? 0 : int((p_start - misc->pre0) / unit0);
         seg.u0 = misc->pre0 + int64_t(seg.hg) * unit0;
         cut(seg, pages_of(seg).np);
-        if (seg.npg == 0) seg = after(seg, seg.b + 1 < p.B ? __ldg(p.context_lens + seg.b + 1) : 0);
+        if (seg.npg == 0) seg = after(seg, seg.b + 1 < p.B ? __ldca(p.context_lens + seg.b + 1) : 0);
         int32_t blk = seg.u0 < p_end ? block_of(seg, 0) : 0;
         while (ok && seg.u0 < p_end) {
             // (as it is: checked where it is used, so that nothing waits for it here)
-            const int32_t L_next = seg.b + 1 < p.B ? __ldg(p.context_lens + seg.b + 1) : 0;
+            const int32_t L_next = seg.b + 1 < p.B ? __ldca(p.context_lens + seg.b + 1) : 0;
             if (lane == 0) {
                 const int s = seg_i % S;
                 if (seg_i >= S) ok = mbar_wait(&segempty[s], ((seg_i / S) - 1) & 1, abort);

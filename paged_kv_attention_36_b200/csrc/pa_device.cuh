@@ -359,6 +359,9 @@ __device__ __forceinline__ uint32_t float2_to_f16x2(float a, float b) {
 }
 
 // ---- data movement and conversion ------------------------------------------
+// Kernels launched as programmatic dependents read tensors with __ldca (an
+// ordinary load): __ldg is for memory that nothing writes during the kernel's
+// life, which begins here before the kernel ahead has ended.
 __device__ __forceinline__ uint4 lds128(const void* smem) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"

@@ -149,14 +149,14 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
     const TileOfCta cta(p, int(SPLIT ? blockIdx.x / cluster_size() : blockIdx.x));
     const int b = cta.b, tile = cta.tile, g = cta.g;
     const bool report = tile == 0 && g == 0 && threadIdx.x == 0;
-    int L = __ldg(p.context_lens + b);
+    int L = __ldca(p.context_lens + b);
     const int64_t cap = int64_t(p.M) * 16;
     if (L < 0 || L > cap) {
         if (report) raise_error(PA_DEVERR_CONTEXT);
         L = L < 0 ? 0 : int32_t(cap);
     }
-    const int q0 = __ldg(p.cu_q_lens + b);
-    int32_t q_len = __ldg(p.cu_q_lens + b + 1) - q0;
+    const int q0 = __ldca(p.cu_q_lens + b);
+    int32_t q_len = __ldca(p.cu_q_lens + b + 1) - q0;
     if (q_len < 0 || q_len > L) {
         if (report) raise_error(PA_DEVERR_CONTEXT);
         q_len = q_len < 0 ? 0 : L;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
     // (masked, and not multiplied)
     auto tile_of = [&](int pg) -> int {
         if (pg >= pages) pg = pages - 1;
-        int32_t blk = __ldg(bt + (pg < ns ? pg : pg + skip));
+        int32_t blk = __ldca(bt + (pg < ns ? pg : pg + skip));
         if (blk < 0 || blk >= p.NB) {
             raise_error(PA_DEVERR_BLOCK_ID);
             blk = 0;
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
         auto fetch = [&](const int8_t* cache, const int (&t)[NP], uint4 (&r)[NP]) {
 #pragma unroll
             for (int i = 0; i < NP; ++i)
-                r[i] = __ldg(reinterpret_cast<const uint4*>(cache + int64_t(t[i]) * (16 * D) + off));
+                r[i] = __ldca(reinterpret_cast<const uint4*>(cache + int64_t(t[i]) * (16 * D) + off));
         };
         tiles_of(0, tl);
         fetch(pp.k_cache, tl, kr);
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
             float top = 0.f;
 #pragma unroll
             for (int ch = 0; ch < D / 8; ++ch) {
-                qv[ch] = valid ? __ldg(src + ch) : make_uint4(0u, 0u, 0u, 0u);
+                qv[ch] = valid ? __ldca(src + ch) : make_uint4(0u, 0u, 0u, 0u);
                 const uint32_t w[4] = {qv[ch].x, qv[ch].y, qv[ch].z, qv[ch].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
         // lane i of each warp holds page i % 4's scales, read one block ahead
         auto page_tile = [&](int j) { return tile_of(j * Cfg::kPages + (lane & (Cfg::kPages - 1))); };
         const int tl = page_tile(0);
-        float ks_next = __ldg(pp.k_scale + tl), vs_next = __ldg(pp.v_scale + tl);
+        float ks_next = __ldca(pp.k_scale + tl), vs_next = __ldca(pp.v_scale + tl);
         int tl_next = page_tile(1);
 
         float m = -INFINITY, l = 0.f;
@@ -420,8 +420,8 @@ __global__ void __launch_bounds__(I8PrefillCfg<D>::kThreads, 2) prefill_i8_kerne
         for (int j = 0; j < nblk; ++j) {
             const int bb = j % NS, n0 = j * BN;
             const float ks = ks_next, vs = vs_next;
-            ks_next = __ldg(pp.k_scale + tl_next);
-            vs_next = __ldg(pp.v_scale + tl_next);
+            ks_next = __ldca(pp.k_scale + tl_next);
+            vs_next = __ldca(pp.v_scale + tl_next);
             tl_next = page_tile(j + 2);
             // a scale of 0: codes of 0, weight still in l; NaN stays
             const float lvl = vs <= 0x1p-100f ? -100.f : __log2f(vs);

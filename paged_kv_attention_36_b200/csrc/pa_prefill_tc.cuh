@@ -68,7 +68,7 @@ struct TileOfCta {
         b = r / p.tiles_per_seq;
         tile = p.tiles_per_seq - 1 - (r - b * p.tiles_per_seq);
         if (p.B <= 32) {
-            const int32_t mine = lane < p.B ? __ldg(p.context_lens + lane) : -1;
+            const int32_t mine = lane < p.B ? __ldca(p.context_lens + lane) : -1;
             int longer = 0;  // sequences before this lane's
             for (int i = 0; i < p.B; ++i) {
                 const int32_t other = __shfl_sync(0xffffffffu, mine, i);
@@ -293,14 +293,14 @@ __device__ __forceinline__ bool tc_attention_tile(const Params& p) {
         }
         if (b >= p.B) return false;
         const bool report = tile == 0 && g == 0 && threadIdx.x == 0;
-        L = __ldg(p.context_lens + b);
+        L = __ldca(p.context_lens + b);
         const int64_t cap = int64_t(p.M) * 16;
         if (L < 0 || L > cap) {
             if (report) raise_error(PA_DEVERR_CONTEXT);
             L = L < 0 ? 0 : int32_t(cap);
         }
-        q0 = __ldg(p.cu_q_lens + b);
-        int32_t q_len = __ldg(p.cu_q_lens + b + 1) - q0;
+        q0 = __ldca(p.cu_q_lens + b);
+        int32_t q_len = __ldca(p.cu_q_lens + b + 1) - q0;
         if (q_len < 0 || q_len > L) {  // queries must be cached tokens of the sequence
             if (report) raise_error(PA_DEVERR_CONTEXT);
             q_len = q_len < 0 ? 0 : L;
@@ -370,7 +370,7 @@ __device__ __forceinline__ bool tc_attention_tile(const Params& p) {
     // Loads in flight while the barriers and TMEM are set up: the page ids of
     // block 0 (producer lanes) and this thread's Q row (softmax warps).
     auto listed = [&](int pg) { return WINDOW && pg >= ns ? pg + skip : pg; };  // table entry of staged page pg
-    const int32_t blk_first = (warp == 0 && lane < Cfg::kPages && lane < pages) ? __ldg(bt + listed(lane)) : 0;
+    const int32_t blk_first = (warp == 0 && lane < Cfg::kPages && lane < pages) ? __ldca(bt + listed(lane)) : 0;
     uint4 qv[D / 8];
     if (warp >= 2) {
         const int r = row0 + (warp & 3) * 32 + lane;
@@ -379,7 +379,7 @@ __device__ __forceinline__ bool tc_attention_tile(const Params& p) {
         const int64_t orow = valid ? (qrow * p.Hq + g * G + r % G) * D : 0;
         const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * 2);
 #pragma unroll
-        for (int ch = 0; ch < D / 8; ++ch) qv[ch] = valid ? __ldg(src + ch) : make_uint4(0u, 0u, 0u, 0u);
+        for (int ch = 0; ch < D / 8; ++ch) qv[ch] = valid ? __ldca(src + ch) : make_uint4(0u, 0u, 0u, 0u);
     }
 
     if (threadIdx.x == 0) {
@@ -448,7 +448,7 @@ __device__ __forceinline__ bool tc_attention_tile(const Params& p) {
         // overlaps the waits)
         auto page_of = [&](int t) -> int32_t {
             const int pg = t * Cfg::kPages + lane;
-            return (t < nblk && lane < Cfg::kPages && pg < pages) ? __ldg(bt + listed(pg)) : 0;
+            return (t < nblk && lane < Cfg::kPages && pg < pages) ? __ldca(bt + listed(pg)) : 0;
         };
         // K runs one block ahead of V: V_j is read one softmax step after K_j
         int nk = 0, nv = 0;  // blocks whose K (V) copies were issued

@@ -50,7 +50,7 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
 // The table row of token t's position (its own row 0, with an error, if the
 // position has none).
 __device__ __forceinline__ const float* angles(const RopeParams& p, int64_t t, bool report) {
-    int32_t pos = __ldg(p.positions + t);
+    int32_t pos = __ldca(p.positions + t);
     if (pos < 0 || pos >= p.max_position) {
         if (report) raise_error(PA_DEVERR_POSITION);
         pos = 0;
@@ -106,7 +106,7 @@ __device__ __forceinline__ void turn_chunks(uint4& lo, uint4& hi, const float (&
 // the HP rows, and the rows' loads are in flight together.
 template <int HP>
 __device__ __forceinline__ void rope_rows(const RopeParams& p, int t, int h0, int heads, int c) {
-    const int32_t slot = __ldg(p.slot_mapping + t);
+    const int32_t slot = __ldca(p.slot_mapping + t);
     const ChunkPair cp = chunk_pair(c, p.rd, p.interleaved);
     if (slot < 0) return;  // padding
     const int32_t block = slot / p.bs, offset = slot - block * p.bs;
@@ -140,8 +140,8 @@ __device__ __forceinline__ void rope_rows(const RopeParams& p, int t, int h0, in
         float cs[8], sn[8];
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
-            const float4 x = __ldg(reinterpret_cast<const float4*>(a + i));
-            const float4 y = __ldg(reinterpret_cast<const float4*>(a + p.rd / 2 + i));
+            const float4 x = __ldca(reinterpret_cast<const float4*>(a + i));
+            const float4 y = __ldca(reinterpret_cast<const float4*>(a + p.rd / 2 + i));
             cs[i] = x.x, cs[i + 1] = x.y, cs[i + 2] = x.z, cs[i + 3] = x.w;
             sn[i] = y.x, sn[i + 1] = y.y, sn[i + 2] = y.z, sn[i + 3] = y.w;
         }
@@ -464,8 +464,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_i8_kernel(const _
     // block cannot be its first.  Every warp sees the same mask.
     const int lane = threadIdx.x & 31, t0 = int(blockIdx.x) / p.parts * p.tokens_per_cta;
     const bool here = lane < p.tokens_per_cta && t0 + lane < p.T;
-    const int32_t my_slot = here ? __ldg(p.slot_mapping + t0 + lane) : -1;
-    const int32_t before = here && t0 + lane > 0 ? __ldg(p.slot_mapping + t0 + lane - 1) : -1;
+    const int32_t my_slot = here ? __ldca(p.slot_mapping + t0 + lane) : -1;
+    const int32_t before = here && t0 + lane > 0 ? __ldca(p.slot_mapping + t0 + lane - 1) : -1;
     bool candidate = my_slot >= 0;
     if (candidate && my_slot / 16 >= p.NB) {
         if (threadIdx.x < 32) raise_error(PA_DEVERR_SLOT);
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_i8_kernel(const _
         const int whole = vec ? p.T / 4 : 0;
 #pragma unroll 8
         for (int u = threadIdx.x; u < whole; u += kRopeThreads) {
-            const int4 s = __ldg(reinterpret_cast<const int4*>(p.slot_mapping) + u);
+            const int4 s = __ldca(reinterpret_cast<const int4*>(p.slot_mapping) + u);
             if (uint32_t(s.x) >> 4 != uint32_t(block) && uint32_t(s.y) >> 4 != uint32_t(block) &&
                 uint32_t(s.z) >> 4 != uint32_t(block) && uint32_t(s.w) >> 4 != uint32_t(block))
                 continue;
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_append_i8_kernel(const _
             look(4 * u + 2, s.z);
             look(4 * u + 3, s.w);
         }
-        for (int u = 4 * whole + threadIdx.x; u < p.T; u += kRopeThreads) look(u, __ldg(p.slot_mapping + u));
+        for (int u = 4 * whole + threadIdx.x; u < p.T; u += kRopeThreads) look(u, __ldca(p.slot_mapping + u));
         __syncthreads();
         if (not_first) continue;
         // the angles of the block's rows, for every head; they land with the first tile
