@@ -177,6 +177,17 @@ def alloc_workspace(dims: pa_dims, num_ctas: int = 0, device=None) -> torch.Tens
                        device=device if device is not None else torch.device("cuda"))
 
 
+def _workspace(workspace, nbytes, sizes, device, stream):
+    """The caller's workspace, checked, or a zero-filled one of ``nbytes(*sizes)`` bytes made on
+    the call's stream: the zeros come before the call, and the allocator hands the memory on
+    only in that stream's order, so the tensor may go as soon as the call is launched."""
+    if workspace is None:
+        with torch.cuda.stream(stream):  # None: the current one
+            workspace = torch.zeros(nbytes(*sizes), dtype=torch.uint8, device=device)
+    _need(workspace, torch.uint8, "workspace", 1)
+    return workspace
+
+
 def pa_cache_append(k_new, v_new, slot_mapping, k_cache, v_cache, stream=None) -> None:
     """k_cache[s // bs][g][s % bs] = k_new[t][g] (v likewise) for s = slot_mapping[t] >= 0."""
     for t, n in ((k_new, "k_new"), (v_new, "v_new")):
@@ -213,9 +224,7 @@ def pa_decode(q, k_cache, v_cache, block_tables, context_lens, scale: float, out
     zero-initialised uint8 device tensor of pa_decode_workspace_bytes(dims)
     bytes; one is allocated when omitted."""
     dims = _decode_args(q, k_cache, v_cache, block_tables, context_lens, out)
-    if workspace is None:
-        workspace = alloc_workspace(dims, device=q.device)
-    _need(workspace, torch.uint8, "workspace", 1)
+    workspace = _workspace(workspace, pa_decode_workspace_bytes, (dims,), q.device, stream)
     _check(lib.pa_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
                          _ptr(context_lens), float(scale), _ptr(out), ctypes.byref(dims),
                          _ptr(workspace), workspace.numel(), _stream(stream)), "pa_decode")
@@ -238,9 +247,7 @@ def pa_append_decode(k_new, v_new, slot_mapping, q, k_cache, v_cache, block_tabl
     (see include/pa.h)."""
     dims = _decode_args(q, k_cache, v_cache, block_tables, context_lens, out)
     T = _append_args(k_new, v_new, slot_mapping, k_cache, v_cache)
-    if workspace is None:
-        workspace = alloc_workspace(dims, device=q.device)
-    _need(workspace, torch.uint8, "workspace", 1)
+    workspace = _workspace(workspace, pa_decode_workspace_bytes, (dims,), q.device, stream)
     _check(lib.pa_append_decode(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), T, _ptr(q),
                                 _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
                                 float(scale), _ptr(out), ctypes.byref(dims), _ptr(workspace),
@@ -319,10 +326,8 @@ def _shared_prefix_call(k_new, v_new, slot_mapping, q, k_cache, v_cache, block_t
     if slot_mapping is not None:
         T = _append_args(k_new, v_new, slot_mapping, k_cache, v_cache)
     ng = _prefix_args(group_offsets, group_prefix_pages, max_group_size)
-    if workspace is None:
-        workspace = torch.zeros(pa_decode_shared_prefix_workspace_bytes(dims, ng, max_group_size),
-                                dtype=torch.uint8, device=q.device)
-    _need(workspace, torch.uint8, "workspace", 1)
+    workspace = _workspace(workspace, pa_decode_shared_prefix_workspace_bytes, (dims, ng, max_group_size), q.device,
+                           stream)
     args = (_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), T, _ptr(q), _ptr(k_cache), _ptr(v_cache),
             _ptr(block_tables), _ptr(context_lens), float(scale), _ptr(group_offsets),
             _ptr(group_prefix_pages), ng, int(max_group_size), _ptr(out), ctypes.byref(dims),
@@ -404,9 +409,7 @@ def pa_decode_fp8(q, k_cache8, v_cache8, k_scale, v_scale, block_tables, context
                   workspace=None, stream=None) -> None:
     """Paged decode over fp8 (E4M3) caches with per-kv-head scales."""
     dims = _decode_fp8_args(q, k_cache8, v_cache8, k_scale, v_scale, block_tables, context_lens, out)
-    if workspace is None:
-        workspace = alloc_workspace(dims, device=q.device)
-    _need(workspace, torch.uint8, "workspace", 1)
+    workspace = _workspace(workspace, pa_decode_workspace_bytes, (dims,), q.device, stream)
     _check(lib.pa_decode_fp8(_ptr(q), _ptr(k_cache8), _ptr(v_cache8), _ptr(k_scale), _ptr(v_scale),
                              _ptr(block_tables), _ptr(context_lens), float(scale), _ptr(out), ctypes.byref(dims),
                              _ptr(workspace), workspace.numel(), _stream(stream)), "pa_decode_fp8")
@@ -429,9 +432,7 @@ def pa_append_decode_fp8(k_new, v_new, slot_mapping, q, k_cache8, v_cache8, k_sc
     """pa_cache_append_fp8 then pa_decode_fp8, fused into one launch."""
     dims, T = _append_decode_fp8_args(k_new, v_new, slot_mapping, q, k_cache8, v_cache8, k_scale, v_scale,
                                       block_tables, context_lens, out)
-    if workspace is None:
-        workspace = alloc_workspace(dims, device=q.device)
-    _need(workspace, torch.uint8, "workspace", 1)
+    workspace = _workspace(workspace, pa_decode_workspace_bytes, (dims,), q.device, stream)
     _check(lib.pa_append_decode_fp8(_ptr(k_new), _ptr(v_new), _ptr(slot_mapping), T, _ptr(q), _ptr(k_cache8),
                                     _ptr(v_cache8), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
                                     _ptr(context_lens), float(scale), _ptr(out), ctypes.byref(dims), _ptr(workspace),
@@ -564,9 +565,7 @@ def _attend(fn, what, q, caches, scales, block_tables, context_lens, scale, wind
             dims = _decode_args(q, k_cache, v_cache, block_tables, context_lens, out)
         elif q.shape[0] != dims.num_seqs:
             raise ValueError("a decode has one query row per sequence")
-        if workspace is None:
-            workspace = alloc_workspace(dims, device=q.device)
-        _need(workspace, torch.uint8, "workspace", 1)
+        workspace = _workspace(workspace, pa_decode_workspace_bytes, (dims,), q.device, stream)
         head, tail = (_ptr(q),), (_ptr(workspace), workspace.numel())
     else:
         if not scales:
