@@ -49,6 +49,7 @@
 // probability.
 #pragma once
 
+#include "pa_cluster.cuh"
 #include "pa_prefill.cuh"
 #include "pa_tcgen05.cuh"
 #include "pa_window.cuh"
@@ -88,7 +89,6 @@ struct TileOfCta {
 // 64 us by 8, 29 and 45 us by 16.  With CTAs two to an SM, runs of 2 blocks or more: 8 rows over 256 tokens
 // 10.7 and 13.2 us in place of 9.3 and 11.9, over 512 11.7 and 13.7 in place of
 // 12.8 and 15.7.
-constexpr int kSplitMinBlocks = 4, kMaxRanks = 16;
 struct KeySplit {
     int ranks, per;  // CTAs that have blocks, blocks of each but the last
     __device__ __forceinline__ explicit KeySplit(int nblk) {

@@ -5,6 +5,7 @@
 
 #include <type_traits>
 
+#include "pa_cluster.cuh"
 #include "pa_decode_wide.cuh"
 #include "pa_host.cuh"
 #include "pa_prefill_i8.cuh"
@@ -187,109 +188,103 @@ pa_status decode_wide(const Call& c, void* workspace, size_t workspace_bytes, vo
     return by_shape(*c.dims, DecodeWide<I8>{p, grid, static_cast<cudaStream_t>(stream)});
 }
 
-// CTAs that share a tile's key blocks: two while they fit two per SM, more (to
-// kMaxRanks) while they fit one per SM, as long as the longest row that the tables
-// and the window allow gives each its blocks.  The lengths are on the device, so
-// wide tables cost short contexts the larger launch.  Measured without and with
-// it, bf16 and 8-bit cache, 32/8 heads of 128: one token over 16,000 tokens 238
-// and 356 -> 29 and 45 us; 16 sequences of 4 rows over 2,000 38 and 66 -> 31 and
-// 45 us; heads of 64 over 60 tokens of 65,536 possible 6.3 and 7.2 -> 8.2 and 9.7
-// us.  Two per SM beyond two ranks: 16.8 in place of 14.6 us for 8 sequences of 16
-// rows over 500 tokens (13.1 us unsplit), 13.5 in place of 14.7 us over 1,000.
-unsigned key_cluster(const Call& c, unsigned tiles, int64_t sms) {
-    const pa_dims& d = *c.dims;
-    int64_t keys = int64_t(d.max_blocks_per_seq) * kBlockSize;
+// Key blocks of the longest row that the tables and the window allow.
+int64_t key_blocks(const Call& c) {
+    int64_t keys = int64_t(c.dims->max_blocks_per_seq) * kBlockSize;
     const int64_t seen = int64_t(c.window) + c.sinks + c.max_q_len;
     if (seen < keys) keys = seen;
-    const int64_t blocks = (keys + 63) / 64;
-    unsigned n = 1;
-    while (n < pa::kMaxRanks && int64_t(tiles) * n * 2 <= (n == 1 ? 2 * sms : sms) &&
-           blocks >= int64_t(n) * 2 * pa::kSplitMinBlocks)
-        n *= 2;
-    return n;
+    return (keys + 63) / 64;
 }
 
-// Shared memory that leaves a CTA its SM to itself.  A cluster's CTAs are placed
-// two to an SM otherwise, where they share the issue slots while other SMs idle:
-// 8-bit cache, one sequence of 4 rows over 16,000 tokens, 4 heads of 128, 35.5 us,
-// alone 30.2 us; 4 of 4 rows over 8,000, 8 heads, 67.7 and 53.3 us.  Only where the
-// GPU's SM clusters hold all of a call's at once (8 of 16 CTAs do not fit on 148
-// SMs: 61.9 us in two turns, 45.1 us two to an SM).
-constexpr int kAloneSmem = 122880;
+constexpr int kAloneSmem = 122880;  // shared memory that leaves a CTA its SM to itself
 
+// Clusters of n CTAs of a kernel that the current device holds at once; asked once
+// per kernel, size and device (`cache`, 0: not asked yet, -1: none).
+using HeldCache = std::atomic<int>[kMaxDevices * 16];
 template <class Kernel>
-bool fits_alone(Kernel kern, int threads, unsigned tiles, unsigned cluster, std::atomic<int>* clusters_held) {
-    std::atomic<int>& held = clusters_held[current_device() * 8 + floor_log2(int(cluster))];  // 0: not asked yet
-    int n = held.load(std::memory_order_relaxed);
-    if (n == 0) {
+int clusters_held(Kernel kern, int threads, int smem, unsigned n, bool alone, HeldCache& cache) {
+    std::atomic<int>& held = cache[(current_device() * 8 + floor_log2(int(n))) * 2 + alone];
+    int count = held.load(std::memory_order_relaxed);
+    if (count == 0) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(cluster);
+        cfg.gridDim = dim3(n);
         cfg.blockDim = dim3(unsigned(threads));
-        cfg.dynamicSmemBytes = kAloneSmem;
+        cfg.dynamicSmemBytes = size_t(alone ? kAloneSmem : smem);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = cluster;
+        attr[0].val.clusterDim.x = n;
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        int found = 0;
-        if (cudaOccupancyMaxActiveClusters(&found, kern, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&count, kern, &cfg) != cudaSuccess) {
             cudaGetLastError();
-            found = 0;
+            count = 0;
         }
-        n = found > 0 ? found : -1;
-        held.store(n, std::memory_order_relaxed);
+        if (count <= 0) count = -1;
+        held.store(count, std::memory_order_relaxed);
     }
-    return n > 0 && tiles <= unsigned(n);
+    return count > 0 ? count : 0;
+}
+
+// Launches `whole`, a kernel with a CTA a tile, or `split`, with a cluster a tile.
+template <class Kernel, class Params>
+pa_status launch_tiles(Kernel whole, Kernel split, int threads, int smem, unsigned tiles, int64_t blocks, int sms,
+                       unsigned* whole_done, unsigned* split_done, HeldCache& cache, cudaStream_t stream,
+                       const Params& p) {
+    if (pa::wanted_ranks(tiles, blocks, sms) > 1) {
+        if (!set_smem_once(split, kAloneSmem, split_done, true)) return PA_ERR_CUDA;
+        const pa::ClusterChoice c = pa::choose_cluster(tiles, blocks, sms, [&](unsigned n, bool alone) -> int64_t {
+            return clusters_held(split, threads, smem, n, alone, cache);
+        });
+        if (c.ranks > 1)
+            return launch_dependent(split, dim3(tiles * c.ranks), threads, c.alone ? kAloneSmem : smem, stream, p,
+                                    c.ranks);
+    }
+    if (!set_smem_once(whole, smem, whole_done)) return PA_ERR_CUDA;
+    return launch_dependent(whole, dim3(tiles), threads, smem, stream, p);
 }
 
 struct PrefillWindow {
     const pa::PrefillParams& p;
-    unsigned tiles, cluster;
+    unsigned tiles;
+    int64_t blocks;
+    int sms;
     cudaStream_t stream;
-    template <int D, int G, bool SPLIT>
-    pa_status run() const {
-        using S = TcShape<D, 64>;
-        auto kern = pa::prefill_tc_kernel<D, G, 64, S::KS, S::CPS, S::NS, true, SPLIT>;
-        static unsigned attr_done[kMaxDevices];
-        if (!set_smem_once(kern, SPLIT ? kAloneSmem : S::Cfg::kWindowSmemBytes, attr_done, SPLIT)) return PA_ERR_CUDA;
-        static_assert(S::Cfg::kWindowSmemBytes <= kAloneSmem);
-        static std::atomic<int> held[kMaxDevices * 8];
-        const bool alone = SPLIT && fits_alone(kern, S::Cfg::kThreads, tiles, cluster, held);
-        const int smem = alone ? kAloneSmem : S::Cfg::kWindowSmemBytes;
-        return launch_dependent(kern, dim3(tiles * cluster), S::Cfg::kThreads, smem, stream, p, cluster);
-    }
     template <int D, int G>
     pa_status operator()() const {
-        return cluster > 1 ? run<D, G, true>() : run<D, G, false>();
+        using S = TcShape<D, 64>;
+        static_assert(S::Cfg::kWindowSmemBytes <= kAloneSmem);
+        static unsigned done[2][kMaxDevices];
+        static HeldCache held;
+        return launch_tiles(pa::prefill_tc_kernel<D, G, 64, S::KS, S::CPS, S::NS, true, false>,
+                            pa::prefill_tc_kernel<D, G, 64, S::KS, S::CPS, S::NS, true, true>, S::Cfg::kThreads,
+                            S::Cfg::kWindowSmemBytes, tiles, blocks, sms, done[0], done[1], held, stream, p);
     }
 };
 
 struct PrefillI8 {
     const pa::PrefillI8Params& p;
-    unsigned tiles, cluster;
+    unsigned tiles;
+    int64_t blocks;
+    int sms;
     cudaStream_t stream;
-    template <int D, int G, bool SPLIT>
-    pa_status run() const {
-        using Cfg = pa::I8PrefillCfg<D>;
-        auto kern = pa::prefill_i8_kernel<D, G, SPLIT>;
-        // the kernel's setmaxnreg split needs exactly the registers it counts on
-        static const bool regs_ok = [&] {
-            cudaFuncAttributes a;
-            return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs == Cfg::kRegs;
-        }();
-        static unsigned attr_done[kMaxDevices];
-        if (!regs_ok || !set_smem_once(kern, SPLIT ? kAloneSmem : Cfg::kSmemBytes, attr_done, SPLIT)) return PA_ERR_CUDA;
-        static_assert(Cfg::kSmemBytes <= kAloneSmem);
-        static std::atomic<int> held[kMaxDevices * 8];
-        const bool alone = SPLIT && fits_alone(kern, Cfg::kThreads, tiles, cluster, held);
-        const int smem = alone ? kAloneSmem : Cfg::kSmemBytes;
-        return launch_dependent(kern, dim3(tiles * cluster), Cfg::kThreads, smem, stream, p, cluster);
-    }
     template <int D, int G>
     pa_status operator()() const {
-        return cluster > 1 ? run<D, G, true>() : run<D, G, false>();
+        using Cfg = pa::I8PrefillCfg<D>;
+        static_assert(Cfg::kSmemBytes <= kAloneSmem);
+        const auto whole = pa::prefill_i8_kernel<D, G, false>, split = pa::prefill_i8_kernel<D, G, true>;
+        // the kernels' setmaxnreg split needs exactly the registers it counts on
+        static const bool regs_ok = [&] {
+            cudaFuncAttributes a, b;
+            return cudaFuncGetAttributes(&a, whole) == cudaSuccess && a.numRegs == Cfg::kRegs &&
+                   cudaFuncGetAttributes(&b, split) == cudaSuccess && b.numRegs == Cfg::kRegs;
+        }();
+        if (!regs_ok) return PA_ERR_CUDA;
+        static unsigned done[2][kMaxDevices];
+        static HeldCache held;
+        return launch_tiles(whole, split, Cfg::kThreads, Cfg::kSmemBytes, tiles, blocks, sms, done[0], done[1], held,
+                            stream, p);
     }
 };
 
@@ -457,7 +452,7 @@ pa_status pa_prefill_window(const void* q, const int32_t* cu_q_lens, int32_t max
         return PA_ERR_CUDA;
     fill_prefill(c, p);
     const unsigned tiles = unsigned(d.num_seqs * p.tiles_per_seq * d.num_kv_heads);
-    return by_shape(d, PrefillWindow{p, tiles, key_cluster(c, tiles, sms), static_cast<cudaStream_t>(stream)});
+    return by_shape(d, PrefillWindow{p, tiles, key_blocks(c), sms, static_cast<cudaStream_t>(stream)});
 }
 
 pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_len, const void* k_cache,
@@ -479,7 +474,7 @@ pa_status pa_prefill_i8(const void* q, const int32_t* cu_q_lens, int32_t max_q_l
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     const unsigned tiles = unsigned(dims->num_seqs * p.a.tiles_per_seq * dims->num_kv_heads);
-    return by_shape(*dims, PrefillI8{p, tiles, key_cluster(c, tiles, sms), static_cast<cudaStream_t>(stream)});
+    return by_shape(*dims, PrefillI8{p, tiles, key_blocks(c), sms, static_cast<cudaStream_t>(stream)});
 }
 
 pa_status pa_rope_append(const void* q, int64_t q_stride, const void* k_new, int64_t k_stride, const void* v_new,
