@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import subprocess
 import sys
 import tempfile
@@ -21,6 +22,11 @@ FLAGS = [
 # translation units, compiled side by side
 UNITS = ("pa_api.cu", "pa_serving.cu")
 
+# Kernels that must be launched with exactly so many registers a thread: their
+# setmaxnreg split gives away and takes what the launch allots (kRegs of
+# csrc/pa_prefill_i8.cuh).  Another compiler's choice fails the build, not the calls.
+REGISTERS = {"prefill_i8_kernel": 80}
+
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
@@ -34,6 +40,23 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def check_registers(ptxas_log: str) -> int:
+    """Reads what ptxas -v says; raises if a kernel of REGISTERS has another
+    number.  Returns how many kernels it checked."""
+    checked = 0
+    for entry in ptxas_log.split("Compiling entry function '")[1:]:
+        name = entry.split("'", 1)[0]
+        for part, want in REGISTERS.items():
+            if part not in name:
+                continue
+            used = re.search(r"Used (\d+) registers", entry)
+            if used is None or int(used.group(1)) != want:
+                raise RuntimeError(f"{name} has {used.group(1) if used else 'unknown'} registers, its register "
+                                   f"split needs {want}")
+            checked += 1
+    return checked
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not stale():
         return LIB
@@ -41,14 +64,26 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         running, objects = [], []
         for unit in UNITS:
             objects.append(os.path.join(tmp, unit + ".o"))
-            cmd = [NVCC, *FLAGS, *extra, "-c", os.path.join(CSRC, unit), "-o", objects[-1]]
-            if verbose:
-                cmd.insert(1, "-Xptxas=-v")
+            cmd = [NVCC, "-Xptxas=-v", *FLAGS, *extra, "-c", os.path.join(CSRC, unit), "-o", objects[-1]]
             print(" ".join(cmd), file=sys.stderr)
-            running.append((cmd, subprocess.Popen(cmd)))
-        failed = [(cmd, p.returncode) for cmd, p in running if p.wait() != 0]
-        if failed:
-            raise subprocess.CalledProcessError(failed[0][1], failed[0][0])
+            log = open(os.path.join(tmp, unit + ".log"), "w+")
+            running.append((cmd, log, subprocess.Popen(cmd, stderr=log)))
+        logs = ""
+        for cmd, log, p in running:
+            code = p.wait()
+            log.seek(0)
+            text = log.read()
+            log.close()
+            said = text if verbose or code != 0 else "\n".join(x for x in text.splitlines() if "warning" in x)
+            if said:
+                print(said, file=sys.stderr)
+            if code != 0:
+                for _, _, other in running:
+                    other.wait()
+                raise subprocess.CalledProcessError(code, cmd)
+            logs += text
+        if check_registers(logs) == 0:
+            raise RuntimeError("the compiler's log names no kernel of " + ", ".join(REGISTERS))
         subprocess.run([NVCC, *FLAGS[:2], "-shared", *objects, "-o", LIB], check=True)
     return LIB
 
