@@ -1,5 +1,6 @@
 """Values at the ends of what the 8-bit attention calls take: queries from the
-smallest bf16 to large ones and far from zero mean, blocks of zero keys.  Against the definition in 64
+smallest bf16 to large ones and far from zero mean, blocks of zero keys; and the
+precision that the calls state, bounded element by element.  Against the definition in 64
 bits, with the bounds of the arithmetic that the kernels use."""
 import pytest
 import torch
@@ -95,3 +96,98 @@ def test_prefill_i8_queries_far_from_zero_mean(pa, D):
     q = q.bfloat16()
     want, mean_abs = _want(q, (k, v, ks, vs, bt), n, 1 / 413, 2)
     ref.assert_attention(_multi(pa, q, (k, v, ks, vs, bt), n, 1 / 413, 2), want, mean_abs, MULTI)
+
+
+# ---- the precision that the calls state -------------------------------------------
+
+def _bounds(q, cache, b, n, scale, window, sinks, weight_step, weight_relative, query_step):
+    """The definition of one sequence's last q.shape[0] rows and what the kernels may be off by:
+      2^-8 |out|, its rounding to bf16;
+      each weight times its V scale: weight_step of the row's heaviest and weight_relative of itself;
+      the queries: query_step of the row's largest value, which moves a logit by up to that times
+      |scale| sum |K|, and so every weight and their sum by as much (twice);
+      2^-15 of the mean |V| for 32-bit logits, exponents and sums."""
+    k, v, ks, vs, bt = cache
+    keys, values = ref.values_i8(k, v, ks, vs, bt[b], n)
+    rows, Hq, D = q.shape
+    Hkv = keys.shape[0]
+    G = Hq // Hkv
+    blocks = bt[b, torch.arange(n) // 16].long()
+    unit = vs.double()[blocks].t()  # [Hkv][n]
+    out, tol = (torch.zeros((rows, Hq, D), dtype=torch.float64) for _ in range(2))
+    for i in range(rows):
+        see = ref.visible(n, n - rows + i, window, sinks)
+        x = q[i].double().view(Hkv, G, D)
+        s = torch.einsum("gjd,gtd->gjt", x, keys[:, see]) * scale
+        w = torch.exp(s - s.amax(-1, keepdim=True))
+        l = w.sum(-1, keepdim=True)
+        mean = torch.einsum("gjt,gtd->gjd", w, values[:, see]) / l
+        mean_abs = torch.einsum("gjt,gtd->gjd", w, values[:, see].abs()) / l
+        heaviest = (w * unit[:, None, see]).amax(-1, keepdim=True)
+        codes = (values[:, see].abs() / unit[:, see, None]).sum(1)[:, None]  # sum of |code|
+        logit = abs(scale) * query_step * x.abs().amax(-1, keepdim=True) * keys[:, see].abs().sum(-1).amax(-1)[:, None, None]
+        err = 2.0 ** -8 * mean.abs() + weight_step * heaviest * codes / l + \
+            (weight_relative + 2 * logit + 2.0 ** -15) * mean_abs
+        out[i], tol[i] = mean.reshape(Hq, D), err.reshape(Hq, D)
+    return out, tol + 1e-30
+
+
+def _within(got, want, tol):
+    got = got.double().cpu()
+    assert torch.isfinite(got).all(), "output not finite"
+    worst = ((got - want).abs() / tol).max().item()
+    assert worst <= 1.0, f"error {worst:.2f} times its bound"
+
+
+@pytest.mark.parametrize("sharp", [0.3, 1.0, 3.0])
+@pytest.mark.parametrize("window,sinks", [(ref.ALL, 0), (100, 5)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 64), (8, 1, 64), (16, 4, 128), (3, 3, 128)])
+def test_decode_i8_within_its_stated_precision(pa, Hq, Hkv, D, window, sinks, sharp):
+    # 16-bit fixed point: weights to 2^-17 of the heaviest (of their step, so of the row at most),
+    # queries to half of 1 / 32512 of the row's largest value
+    g = torch.Generator().manual_seed(Hq + D)
+    lens = [1, 16, 40, 64, 200, 777]
+    cache = k, v, ks, vs, bt = ref.i8_batch(g, lens, Hkv, D)
+    q = torch.randn((len(lens), Hq, D), generator=g).bfloat16()
+    scale = sharp * D ** -0.5
+    out = torch.full_like(q, float("nan")).cuda()
+    pa.pa_decode_i8(q.cuda(), *[t.cuda() for t in cache], torch.tensor(lens, dtype=torch.int32).cuda(), scale, out,
+                    window=window, sinks=sinks)
+    for b, n in enumerate(lens):
+        want, tol = _bounds(q[b:b + 1], cache, b, n, scale, window, sinks, 2.0 ** -17, 0.0, 0.5 / 32512)
+        _within(out[b:b + 1], want, tol)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_i8_one_query_channel_far_above_the_rest(pa, D):
+    # a channel 1000 times the others where keys are small: the others keep 2^-16 of that one
+    g = torch.Generator().manual_seed(D)
+    lens = [300, 70]
+    k, v, ks, vs, bt = ref.i8_batch(g, lens, 2, D)
+    k[..., 7] = k[..., 7] // 100
+    q = torch.randn((2, 8, D), generator=g)
+    q[..., 7] *= 1000
+    q = q.bfloat16()
+    out = torch.full_like(q, float("nan")).cuda()
+    pa.pa_decode_i8(q.cuda(), *[t.cuda() for t in (k, v, ks, vs, bt)], torch.tensor(lens, dtype=torch.int32).cuda(),
+                    0.02, out)
+    for b, n in enumerate(lens):
+        want, tol = _bounds(q[b:b + 1], (k, v, ks, vs, bt), b, n, 0.02, ref.ALL, 0, 2.0 ** -17, 0.0, 0.5 / 32512)
+        _within(out[b:b + 1], want, tol)
+    multi = _multi(pa, q[:1], (k, v, ks, vs, bt[:1]), lens[0], 0.02)
+    want, tol = _bounds(q[:1], (k, v, ks, vs, bt), 0, lens[0], 0.02, ref.ALL, 0, 2.0 ** -31, MULTI, 2.0 ** -25)
+    _within(multi, want, tol)
+
+
+@pytest.mark.parametrize("sharp", [0.3, 1.0, 3.0])
+@pytest.mark.parametrize("window,sinks", [(ref.ALL, 0), (100, 5)])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 64), (8, 1, 64), (16, 4, 128), (3, 3, 128)])
+def test_prefill_i8_within_its_stated_precision(pa, Hq, Hkv, D, window, sinks, sharp):
+    # f16 weights, lifted: 2^-11 of each, 2^-31 of the heaviest; queries as f16 of less than 4
+    g = torch.Generator().manual_seed(Hq + D)
+    scale = sharp * D ** -0.5
+    for n, rows in ((90, 90), (777, 30), (2500, 2)):
+        cache = ref.i8_batch(g, [n], Hkv, D)
+        q = torch.randn((rows, Hq, D), generator=g).bfloat16()
+        want, tol = _bounds(q, cache, 0, n, scale, window, sinks, 2.0 ** -31, MULTI, 2.0 ** -25)
+        _within(_multi(pa, q, cache, n, scale, window, sinks), want, tol)
