@@ -411,8 +411,8 @@ PA_API pa_status pa_prefill_window(const void* q, const int32_t* cu_q_lens, int3
  * and scales need no initialisation.  Otherwise, when the scale grows, the
  * block's other codes become round(code * old / scale).  A NaN or infinity
  * poisons its block's values of that head until the block starts anew.
- * Every block looks through the call's slots, which shows from about 32,000
- * tokens on (65,536 tokens of 8 kv heads of 128: 234 us, 131,072: 625 us).
+ * Every block looks through the call's slots, which shows past 65,536 tokens
+ * (of 8 kv heads of 128: 234 us, 131,072 tokens 625 us): cut longer calls.
  *
  * pa_decode_i8, pa_prefill_i8: pa_decode and pa_prefill over these caches,
  * with the window of pa_decode_window (PA_WINDOW_ALL, 0 for none); q must be

@@ -18,11 +18,11 @@ struct ClusterChoice {
 // kMaxRanks) while they fit one per SM, as long as the longest row that the tables
 // and the window allow gives each its blocks.  The lengths are on the device, so
 // wide tables cost short contexts the larger launch.  Measured without and with
-// it, bf16 and 8-bit cache, 32/8 heads of 128: one token over 16,000 tokens 238
-// and 356 -> 29 and 42 us; 16 sequences of 4 rows over 2,000 38 and 66 -> 32 and
-// 41 us; heads of 64 over 60 tokens of 65,536 possible 6.3 and 7.2 -> 8.2 and 9.7
-// us.  Two per SM beyond two ranks: 16.8 in place of 14.6 us for 8 sequences of 16
-// rows over 500 tokens (13.1 us unsplit), 13.5 in place of 14.7 us over 1,000.
+// it, bf16 and 8-bit cache, 32/8 heads of 128: one token over 16,000 tokens 237
+// and 347 -> 29 and 42 us; 16 sequences of 4 rows over 2,000 37 and 54 -> 32 and
+// 41 us; heads of 64 over 60 tokens of 65,536 possible 6.4 and 6.9 -> 8.6 and 9.8
+// us; 8 sequences of 16 rows over 500, heads of 64, 10.9 and 12.2 -> 12.5 and 13.0,
+// over 1,000 16.4 and 19.1 -> 15.1 and 16.4.
 inline unsigned wanted_ranks(unsigned tiles, int64_t blocks, int64_t sms) {
     unsigned n = 1;
     while (n < unsigned(kMaxRanks) && int64_t(tiles) * n * 2 <= (n == 1 ? 2 * sms : sms) &&

@@ -12,7 +12,10 @@
 //                        S_{j+1} is computed while S_j is in the softmax)
 //   P_j = 2^(S_j*c - m)  softmax warpgroup: thread i owns row i (TMEM lane i),
 //                        masks, keeps the running max m and sum l, writes P_j
-//                        as bf16 over the first half of S_j's columns
+//                        as bf16 over the first half of S_j's columns (V is
+//                        bf16, and both operands of an MMA have one type; two
+//                        parts of P would double the MMAs of P V; l sums P
+//                        before that rounding, of 2^-8 at most)
 //   O  += P_j V_j        tcgen05.mma, A = P_j (TMEM), B = V_j (shared memory,
 //                        MN-major), fp32 accumulator in TMEM, one MMA per page
 //
@@ -85,10 +88,8 @@ struct TileOfCta {
 // about 1.5 us, stays below what it saves), and meet in one another's shared
 // memory: no workspace, no second kernel.  Rank r's run starts at block r * per;
 // ranks past the last run leave at once.  Measured, bf16 and 8-bit cache: one
-// token, 32/8 heads of 128, over 16,000: 238 and 356 us by one CTA a tile, 40 and
-// 64 us by 8, 29 and 45 us by 16.  With CTAs two to an SM, runs of 2 blocks or more: 8 rows over 256 tokens
-// 10.7 and 13.2 us in place of 9.3 and 11.9, over 512 11.7 and 13.7 in place of
-// 12.8 and 15.7.
+// token, 32/8 heads of 128, over 16,000: 237 and 347 us by one CTA a tile, 40 and
+// 46 us by 8, 29 and 42 us by 16.
 struct KeySplit {
     int ranks, per;  // CTAs that have blocks, blocks of each but the last
     __device__ __forceinline__ explicit KeySplit(int nblk) {
@@ -244,10 +245,11 @@ struct TcPrefillCfg {
 // sees are streamed, as one list: `ns` pages of sinks, then the pages from the
 // first row's window on, `skip` pages between them left out.  A row sees list
 // keys [0, min(sinks, hi)) and [lo, hi).  Measured: 16 chunks of 512 tokens,
-// window 1024, 4 sinks, 32/8 heads of 64: 122.1 us, 477 TFLOP/s of visible pairs
+// window 1024, 4 sinks, 32/8 heads of 64: 124 us, 468 TFLOP/s of visible pairs
 // (blocks of 64 keys at the window's edges are multiplied whole).
 // SPLIT (WINDOW): a cluster of CTAs on each tile (KeySplit).  A kernel of its own:
-// the same code in the unsplit one costs it registers (127 against 122 us above).
+// the same code in the unsplit one costs it registers (127 against 122 us, without
+// the second pass).
 // SECOND (WINDOW): the pass after one that returned true, in every CTA of the tile
 // (WindowRow); it has the first one's tensor memory and barriers of its own.
 template <bool PREFIX, int D, int G, int BN, int KS, int NS, bool WINDOW = false, bool SPLIT = false,
